@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_gemm_tm.cu", "moe_gemm_tmx.cu", "moe_gemm_pair.cu",
-           "moe_router.cu", "moe_noalloc.cu"]
+           "moe_router.cu", "moe_noalloc.cu", "moe_ops.cu", "moe_grouped.cu", "moe_wgrad.cu", "moe_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

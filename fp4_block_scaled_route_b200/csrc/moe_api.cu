@@ -982,6 +982,26 @@ moe_status moe_set_fault_injection(moe_ctx* c, int mode) {
   return MOE_OK;
 }
 
+moe_status moe_route(moe_ctx* c, int T, const int32_t* ids, int32_t* counts, int32_t* offsets, int32_t* perm,
+                     int32_t* inv, void* stream) {
+  if (!c || T < 0 || T > c->max_T || !counts || !offsets || !aligned(counts, 4) || !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(counts, 0, sizeof(int32_t) * c->NG, s) == cudaSuccess &&
+                   cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (c->NG + 1), s) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  if (!ids || !perm || !inv || !aligned(ids, 4) || !aligned(perm, 4) || !aligned(inv, 4)) return MOE_ERR_INVALID_ARG;
+  RouteParams rp{};
+  rp.T = T; rp.k = c->k; rp.E = c->E; rp.n_shared = c->n_shared;
+  rp.BN = 128;  // the tile list is scratch here
+  rp.ids = ids; rp.counts = counts; rp.offsets = offsets; rp.perm = perm; rp.inv = inv;
+  rp.tiles = c->tiles; rp.num_tiles = c->num_tiles; rp.status = c->status;
+  rp.part = c->route_part;
+  return moe::launch_route(rp, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 moe_status moe_last_config(moe_ctx* c, int* tile_n, int* grid) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (tile_n) *tile_n = c->last_bn;

@@ -1,0 +1,145 @@
+// moe_grouped.cuh -- what the ragged grouped products (moe_grouped.cu,
+// moe_wgrad.cu) share: operand descriptors, pair and cluster PTX, and the
+// table of row tiles that every CTA builds from the groups' offsets.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "moe_internal.h"
+#include "moe_ops.h"
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+// ---- TMA ----------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// ---- operands -----------------------------------------------------------------
+// Shared-memory descriptor of an operand whose M (or N) index is the
+// contiguous one, as TMA writes it with 128-byte swizzle: boxes of 64
+// 16-bit elements along M by `box_rows` contraction rows, each row a 128-byte
+// line.  Eight lines form a 1024-byte core group (stride offset: the next
+// eight contraction rows); the next 64 elements along M start one box later
+// (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t box_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(box_bytes >> 4) << 16;  // leading byte offset: next 64 elements along M
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride byte offset: next 8 contraction rows
+  d |= static_cast<uint64_t>(1) << 46;               // descriptor version for sm_100
+  d |= static_cast<uint64_t>(2) << 61;               // layout: 128-byte swizzle
+  return d;
+}
+
+// Instruction descriptors.  kind::f16 with fp32 accumulation: both operands
+// fp16 (fmt 0) or both bf16 (fmt 1); a_mn / b_mn: that operand's M / N index
+// is contiguous.  kind::i8: signed bytes, int32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fmt, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) |
+         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_s8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_s8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Bounded wait used while draining: like mbar_wait, but blind to the abort word.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitCycles) break;
+}
+
+// Two fp32 values -> two bf16 or fp16 (lo in bits 0-15), each rounded to nearest even once.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---- groups --------------------------------------------------------------------
+// Builds in shared memory the groups' offsets and the first row tile of each
+// group (tiles of `tile_rows` rows).  All THREADS threads of the CTA call it;
+// it ends with a barrier.  offsets == nullptr: one group of all P rows.
+// Returns false when the offsets are unusable (negative, falling, or past P):
+// the caller then computes nothing.
+template <int THREADS>
+__device__ __forceinline__ bool build_group_table(const int32_t* offsets, int E, int P, int tile_rows, int* s_off,
+                                                  int* s_tile, int* s_scan) {
+  static_assert(THREADS % 32 == 0 && THREADS <= 1024, "block");
+  constexpr int NW = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (E + THREADS - 1) / THREADS;  // consecutive groups per thread
+  const int e0 = tid * per;
+  int sum = 0, bad = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = e0 + i;
+    if (e >= E) break;
+    const int lo = offsets ? offsets[e] : 0, hi = offsets ? offsets[e + 1] : P;
+    bad |= (lo < 0) | (hi < lo) | (hi > P);
+    s_off[e] = lo;
+    if (e == E - 1) s_off[E] = hi;
+    s_tile[e + 1] = bad ? 0 : (hi - lo) / tile_rows + ((hi - lo) % tile_rows != 0);
+    sum += s_tile[e + 1];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  bad = __syncthreads_or(bad);
+  int run = incl - sum;
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+    if (w < warp) run += s_scan[w];
+  for (int i = 0; i < per; ++i) {
+    const int e = e0 + i;
+    if (e >= E) break;
+    run += s_tile[e + 1];
+    s_tile[e + 1] = run;
+  }
+  if (tid == 0) s_tile[0] = 0;
+  __syncthreads();
+  return !bad;
+}
+
+}  // namespace moe

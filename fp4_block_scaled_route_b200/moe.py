@@ -10,6 +10,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -25,6 +26,10 @@ MOE_ERR_NO_MEMORY = 4
 MOE_ERR_TIMEOUT = 5
 MOE_ERR_BAD_ROUTING = 6
 
+MOE_DT_BF16 = 0
+MOE_DT_FP16 = 1
+MOE_DT_FP32 = 2
+
 MOE_WFMT_FP8_E4M3_B128 = 0
 MOE_WFMT_MXFP4_E2M1_E8M0_K32 = 1
 MOE_WFMT_NVFP4_E2M1_E4M3_K16 = 2
@@ -34,6 +39,7 @@ MOE_WFMT_MXFP8_E4M3_E8M0_K32 = 4
 # Every entry point declared in include/moe.h: name -> (restype, argtypes)
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "moe_create": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
     "moe_create_ex": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
@@ -59,6 +65,15 @@ SIGNATURES = {
     "moe_green_ctx_sms": (_i, [_vp, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
     "moe_set_dispatch_overlap": (_i, [_vp, _i]),
     "moe_dispatch_overlap_ctas": (_i, [_vp, ctypes.POINTER(_i)]),
+    "moe_route": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_permute": (_i, [_i, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _ll, _vp]),
+    "moe_combine": (_i, [_i, _i, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _vp, _ll, _vp]),
+    "moe_combine_backward": (_i, [_i, _i, _i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp, _vp]),
+    "moe_grouped_gemm": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _vp]),
+    "moe_grouped_gemm_dgrad": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _vp]),
+    "moe_grouped_gemm_wgrad": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp]),
+    "moe_quant_int8": (_i, [_i, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _ll, _vp, _vp]),
+    "moe_int8_gemm": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _vp, _ll, _ll, _vp, _vp, _ll, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -213,6 +228,49 @@ def moe_profile_read(ctx):
     return list(arr), n.value
 
 
+def moe_route(ctx, T, topk_ids, counts, offsets, perm, inv, stream) -> int:
+    return lib().moe_route(ctx, T, topk_ids, counts, offsets, perm, inv, stream)
+
+
+def moe_permute(dtype, rows, H, T, k, x, ldx, perm, y, ldy, stream) -> int:
+    return lib().moe_permute(dtype, rows, H, T, k, x, ldx, perm, y, ldy, stream)
+
+
+def moe_combine(dtype, rows, H, T, k, n_shared, y, ldy, inv, topk_w, out, ldo, stream) -> int:
+    return lib().moe_combine(dtype, rows, H, T, k, n_shared, y, ldy, inv, topk_w, out, ldo, stream)
+
+
+def moe_combine_backward(dtype, rows, H, T, k, n_shared, dout, lddout, y, ldy, inv, topk_w, dy, lddy, dtopk_w,
+                         stream) -> int:
+    return lib().moe_combine_backward(dtype, rows, H, T, k, n_shared, dout, lddout, y, ldy, inv, topk_w, dy, lddy,
+                                      dtopk_w, stream)
+
+
+def moe_grouped_gemm(dtype, out_dtype, E, P, N, K, offsets, x, ldx, w, ldw, stride_w, y, ldy, d_status, stream) -> int:
+    return lib().moe_grouped_gemm(dtype, out_dtype, E, P, N, K, offsets, x, ldx, w, ldw, stride_w, y, ldy, d_status,
+                                  stream)
+
+
+def moe_grouped_gemm_dgrad(dtype, out_dtype, E, P, N, K, offsets, dy, lddy, w, ldw, stride_w, dx, lddx, d_status,
+                           stream) -> int:
+    return lib().moe_grouped_gemm_dgrad(dtype, out_dtype, E, P, N, K, offsets, dy, lddy, w, ldw, stride_w, dx, lddx,
+                                        d_status, stream)
+
+
+def moe_grouped_gemm_wgrad(dtype, out_dtype, E, P, N, K, offsets, dy, lddy, x, ldx, dw, d_status, stream) -> int:
+    return lib().moe_grouped_gemm_wgrad(dtype, out_dtype, E, P, N, K, offsets, dy, lddy, x, ldx, dw, d_status, stream)
+
+
+def moe_quant_int8(dtype, rows, K, T, k, x, ldx, perm, q, ldq, scale, stream) -> int:
+    return lib().moe_quant_int8(dtype, rows, K, T, k, x, ldx, perm, q, ldq, scale, stream)
+
+
+def moe_int8_gemm(out_dtype, E, P, N, K, offsets, q, ldq, q_scale, w, ldw, stride_w, w_scale, y, ldy, d_status,
+                  stream) -> int:
+    return lib().moe_int8_gemm(out_dtype, E, P, N, K, offsets, q, ldq, q_scale, w, ldw, stride_w, w_scale, y, ldy,
+                               d_status, stream)
+
+
 # ---- torch convenience wrapper (marshalling only) ------------------------
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
@@ -337,6 +395,22 @@ class MoeLayer:
                "moe_router_topk")
         return ids, w
 
+    def route(self, topk_ids, stream=None):
+        """Device int32 (counts, offsets, perm, inv) of topk_ids [T, k], in stream order (moe_route)."""
+        import torch
+        T = topk_ids.shape[0]
+        if topk_ids.shape != (T, self.k):
+            raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, {self.k}]")
+        NG, P = self.E + self.n_shared, T * (self.k + self.n_shared)
+        with _launch("route", stream, topk_ids=(topk_ids, torch.int32)) as s:
+            if not topk_ids.is_contiguous():
+                raise ValueError("route: topk_ids is not contiguous")
+            counts, offsets, perm, inv = (torch.empty(n, dtype=torch.int32, device=topk_ids.device)
+                                          for n in (NG, NG + 1, P, P))
+            _check(moe_route(self.ctx, T, _ptr(topk_ids), _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv), s),
+                   "moe_route")
+        return counts, offsets, perm, inv
+
     def set_green_ctx(self, dispatch_sms):
         """Green-Context partition: dispatch kernels on >= dispatch_sms SMs, GEMMs on the rest (0 = off)."""
         _check(moe_set_green_ctx(self.ctx, dispatch_sms), "moe_set_green_ctx")
@@ -375,3 +449,263 @@ def finalize_bf16(acc, out=None, stream=None):
     _check(moe_finalize_bf16(_ptr(acc.contiguous()), _ptr(out), acc.numel(), _stream_handle(stream)),
            "moe_finalize_bf16")
     return out
+
+
+# ---- expert operators on torch tensors (marshalling only) -----------------
+@contextlib.contextmanager
+def _launch(what, stream=None, **tensors):
+    """Checks tensors (name -> tensor, or (tensor, required dtype); None is skipped), makes their device current and
+    `stream` (default: that device's current stream) the one results are allocated on; yields the stream handle."""
+    import torch
+    dev = None
+    for name, t in tensors.items():
+        t, dtype = t if isinstance(t, tuple) else (t, None)
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name} is not a CUDA tensor")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{what}: {name} is on {t.device}, not on {dev}")
+        dev = t.device
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev), contextlib.ExitStack() as stack:
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _dtype_code(dtype, what):
+    import torch
+    codes = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_FP16, torch.float32: MOE_DT_FP32}
+    if dtype not in codes:
+        raise ValueError(f"{what}: type {dtype} is not supported")
+    return codes[dtype]
+
+
+def _new_rows(rows, n, dtype, device):
+    """An unset [rows, n] matrix whose row stride is a multiple of 16 bytes (contiguous where n allows it)."""
+    import torch
+    step = 16 // dtype.itemsize
+    return torch.empty((rows, -(-n // step) * step), dtype=dtype, device=device)[:, :n]
+
+
+def _matrix(t, shape, what):
+    """Row stride in elements of a matrix with contiguous rows; `shape` may hold None for any size."""
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple('any' if n is None else n for n in shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: rows are not contiguous")
+    if t.shape[-2] > 1:
+        return t.stride(-2)
+    step = 16 // t.element_size()      # a single row: its stride is never used
+    return -(-t.shape[-1] // step) * step
+
+
+def _vector(t, n, what):
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
+
+
+def _groups(offsets, E, what):
+    if offsets.dim() != 1 or offsets.shape[0] != E + 1 or not offsets.is_contiguous():
+        raise ValueError(f"{what}: offsets has shape {tuple(offsets.shape)}, not [{E + 1}]")
+
+
+def _weights(w, N, K, what):
+    """(row stride, expert stride) of [E, N, K] weights."""
+    ld = _matrix(w, (None, N, K), what)
+    return ld, (w.stride(0) if w.shape[0] > 1 else 0)
+
+
+def _grouped(entry, what, rows, name, w, offsets, R, M, out, out_dtype, status, stream):
+    import torch
+    P = rows.shape[0]
+    E, N, K = w.shape
+    ld = _matrix(rows, (None, R), f"{what}: {name}")
+    ldw, sw = _weights(w, None, None, f"{what}: w")
+    _groups(offsets, E, what)
+    out_dtype = out.dtype if out is not None else (out_dtype or rows.dtype)
+    dt, odt = _dtype_code(rows.dtype, what), _dtype_code(out_dtype, what)
+    with _launch(what, stream, **{name: rows}, w=(w, rows.dtype), offsets=(offsets, torch.int32), out=out,
+                 status=(status, torch.int32)) as s:
+        if out is None:
+            out = _new_rows(P, M, out_dtype, rows.device)
+        ldo = _matrix(out, (P, M), f"{what}: out")
+        _check(entry(dt, odt, E, P, N, K, _ptr(offsets), _ptr(rows), ld, _ptr(w), ldw, sw, _ptr(out), ldo,
+                     _ptr(status), s), entry.__name__)
+    return out
+
+
+def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=None):
+    """y[p] = x[p] w[e]^T for the rows offsets[e] .. offsets[e+1]-1 of every expert e (moe_grouped_gemm).
+
+    x [P, K] and w [E, N, K] bf16 or fp16 with contiguous rows (any row and expert strides that are multiples of 16
+    bytes), offsets device int32 [E+1]; out [P, N] in the same type or fp32.  Rows outside every group are left as
+    they were (unspecified in an `out` made here).  status: optional device int32, see moe.h."""
+    if w.dim() != 3:
+        raise ValueError(f"grouped_gemm: w has shape {tuple(w.shape)}, not [E, N, K]")
+    return _grouped(moe_grouped_gemm, "grouped_gemm", x, "x", w, offsets, w.shape[2], w.shape[1], out, out_dtype,
+                    status, stream)
+
+
+def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, status=None, stream=None):
+    """dx[p] = dy[p] w[e], the gradient of grouped_gemm for x (moe_grouped_gemm_dgrad): dy [P, N] -> [P, K]."""
+    if w.dim() != 3:
+        raise ValueError(f"grouped_gemm_dgrad: w has shape {tuple(w.shape)}, not [E, N, K]")
+    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", dy, "dy", w, offsets, w.shape[1], w.shape[2], out,
+                    out_dtype, status, stream)
+
+
+def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, stream=None):
+    """dw[e] = sum over the rows of e of dy[p]^T x[p], the gradient of grouped_gemm for w (moe_grouped_gemm_wgrad):
+    dy [P, N], x [P, K] -> [E, N, K], zeros for an expert without rows."""
+    import torch
+    what = "grouped_gemm_wgrad"
+    lddy = _matrix(dy, (None, None), f"{what}: dy")
+    ldx = _matrix(x, (dy.shape[0], None), f"{what}: x")
+    P, N, K, E = dy.shape[0], dy.shape[1], x.shape[1], offsets.shape[0] - 1
+    _groups(offsets, E, what)
+    out_dtype = out.dtype if out is not None else (out_dtype or dy.dtype)
+    dt, odt = _dtype_code(dy.dtype, what), _dtype_code(out_dtype, what)
+    with _launch(what, stream, dy=dy, x=(x, dy.dtype), offsets=(offsets, torch.int32), out=out,
+                 status=(status, torch.int32)) as s:
+        if out is None:
+            out = torch.empty((E, N, K), dtype=out_dtype, device=dy.device)
+        if out.shape != (E, N, K) or not out.is_contiguous():
+            raise ValueError(f"{what}: out is not contiguous [{E}, {N}, {K}]")
+        _check(moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, _ptr(offsets), _ptr(dy), lddy, _ptr(x), ldx, _ptr(out),
+                                      _ptr(status), s), "moe_grouped_gemm_wgrad")
+    return out
+
+
+def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
+    """(q int8 [rows, K], scale fp32 [rows]) of x [T, K] bf16 or fp16, one scale amax / 127 per row (moe_quant_int8).
+    With perm (device int32 [rows]) row p is token perm[p] // k, quantised in expert order."""
+    import torch
+    what = "quant_int8"
+    ldx = _matrix(x, (None, None), f"{what}: x")
+    T, K = x.shape
+    rows = T if perm is None else perm.shape[0]
+    dt = _dtype_code(x.dtype, what)
+    with _launch(what, stream, x=x, perm=(perm, torch.int32), out=(out, torch.int8),
+                 scale=(scale, torch.float32)) as s:
+        if perm is not None:
+            _vector(perm, rows, f"{what}: perm")
+        if out is None:
+            out = _new_rows(rows, K, torch.int8, x.device)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        ldq = _matrix(out, (rows, K), f"{what}: out")
+        _vector(scale, rows, f"{what}: scale")
+        _check(moe_quant_int8(dt, rows, K, T, k, _ptr(x), ldx, _ptr(perm), _ptr(out), ldq, _ptr(scale), s),
+               "moe_quant_int8")
+    return out, scale
+
+
+def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, status=None, stream=None):
+    """y[p, n] = q_scale[p] w_scale[e, n] sum_k q[p, k] w[e, n, k] (moe_int8_gemm).
+
+    q int8 [P, K], q_scale fp32 [P], w int8 [E, N, K] and w_scale fp32 [E, N] (or [N, K] and [N] without offsets: one
+    dense product), offsets device int32 [E+1].  out [P, N] bf16 (default), fp16 or fp32."""
+    import torch
+    what = "int8_gemm"
+    if offsets is None and w.dim() == 2:
+        w = w[None]
+    if w.dim() != 3 or (offsets is None and w.shape[0] != 1):
+        raise ValueError(f"{what}: w has shape {tuple(w.shape)}; one matrix without offsets, [E, N, K] with them")
+    E, N, K = w.shape
+    ldq = _matrix(q, (None, K), f"{what}: q")
+    P = q.shape[0]
+    ldw, sw = _weights(w, None, None, f"{what}: w")
+    if offsets is not None:
+        _groups(offsets, E, what)
+    _vector(q_scale, P, f"{what}: q_scale")
+    _vector(w_scale, E * N, f"{what}: w_scale")
+    out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    odt = _dtype_code(out_dtype, what)
+    with _launch(what, stream, q=(q, torch.int8), q_scale=(q_scale, torch.float32), w=(w, torch.int8),
+                 w_scale=(w_scale, torch.float32), offsets=(offsets, torch.int32), out=out,
+                 status=(status, torch.int32)) as s:
+        if out is None:
+            out = _new_rows(P, N, out_dtype, q.device)
+        ldo = _matrix(out, (P, N), f"{what}: out")
+        _check(moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), _ptr(q), ldq, _ptr(q_scale), _ptr(w), ldw, sw,
+                             _ptr(w_scale), _ptr(out), ldo, _ptr(status), s), "moe_int8_gemm")
+    return out
+
+
+def permute(x, perm, k, out=None, stream=None):
+    """y[p] = x[perm[p] // k]: rows of x [T, H] (bf16, fp16 or fp32) in expert order (moe_permute).  Rows whose slot is
+    -1 are left as they were (unspecified in an `out` made here)."""
+    import torch
+    what = "permute"
+    ldx = _matrix(x, (None, None), f"{what}: x")
+    T, H = x.shape
+    rows = perm.shape[0]
+    dt = _dtype_code(x.dtype, what)
+    with _launch(what, stream, x=x, perm=(perm, torch.int32), out=(out, x.dtype)) as s:
+        _vector(perm, rows, f"{what}: perm")
+        if out is None:
+            out = _new_rows(rows, H, x.dtype, x.device)
+        ldy = _matrix(out, (rows, H), f"{what}: out")
+        _check(moe_permute(dt, rows, H, T, k, _ptr(x), ldx, _ptr(perm), _ptr(out), ldy, s), "moe_permute")
+    return out
+
+
+def _combine_sizes(inv, topk_w, k, n_shared, what):
+    """(T, k) from the slots' count; topk_w [T, k], or None with k given."""
+    if topk_w is not None:
+        if topk_w.dim() != 2 or (k is not None and topk_w.shape[1] != k):
+            raise ValueError(f"{what}: topk_w has shape {tuple(topk_w.shape)}, not [T, k]")
+        T, k = topk_w.shape
+        _vector(topk_w, T * k, f"{what}: topk_w")
+    else:
+        if k is None:
+            raise ValueError(f"{what}: without topk_w, k has to be given")
+        T = inv.numel() // (k + n_shared)
+    _vector(inv, T * (k + n_shared), f"{what}: inv")
+    return T, k
+
+
+def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
+    """out[t] = sum_j topk_w[t, j] y[inv[t*k + j]] (+ the shared expert's row) from y [rows, H] (moe_combine).
+    topk_w fp32 [T, k], or None (ones; then k is given): the gradient of permute."""
+    import torch
+    what = "combine"
+    ldy = _matrix(y, (None, None), f"{what}: y")
+    rows, H = y.shape
+    T, k = _combine_sizes(inv, topk_w, k, n_shared, what)
+    dt = _dtype_code(y.dtype, what)
+    with _launch(what, stream, y=y, inv=(inv, torch.int32), topk_w=(topk_w, torch.float32), out=(out, y.dtype)) as s:
+        if out is None:
+            out = _new_rows(T, H, y.dtype, y.device)
+        ldo = _matrix(out, (T, H), f"{what}: out")
+        _check(moe_combine(dt, rows, H, T, k, n_shared, _ptr(y), ldy, _ptr(inv), _ptr(topk_w), _ptr(out), ldo, s),
+               "moe_combine")
+    return out
+
+
+def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, stream=None):
+    """(dy, dtopk_w): gradients of combine for y and topk_w (moe_combine_backward).  Rows of dy that no slot names are
+    left as they were (unspecified in a `dy` made here)."""
+    import torch
+    what = "combine_backward"
+    T, k = _combine_sizes(inv, topk_w, None, n_shared, what)
+    ldy = _matrix(y, (None, None), f"{what}: y")
+    rows, H = y.shape
+    ldd = _matrix(dout, (T, H), f"{what}: dout")
+    dt = _dtype_code(y.dtype, what)
+    with _launch(what, stream, y=y, dout=(dout, y.dtype), inv=(inv, torch.int32), topk_w=(topk_w, torch.float32),
+                 dy=(dy, y.dtype), dtopk_w=(dtopk_w, torch.float32)) as s:
+        if dy is None:
+            dy = _new_rows(rows, H, y.dtype, y.device)
+        if dtopk_w is None:
+            dtopk_w = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        lddy = _matrix(dy, (rows, H), f"{what}: dy")
+        _vector(dtopk_w, T * k, f"{what}: dtopk_w")
+        _check(moe_combine_backward(dt, rows, H, T, k, n_shared, _ptr(dout), ldd, _ptr(y), ldy, _ptr(inv),
+                                    _ptr(topk_w), _ptr(dy), lddy, _ptr(dtopk_w), s), "moe_combine_backward")
+    return dy, dtopk_w

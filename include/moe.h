@@ -411,6 +411,115 @@ moe_status moe_forward_noalloc(int H, int I, int E, int k, int wfmt, int n_share
                                const int32_t* topk_ids, const float* topk_w, const void* w13, const void* s13,
                                const void* w2, const void* s2, void* out, int32_t* d_status, void* stream);
 
+/* ---- Expert operators -------------------------------------------------------
+ * The layer's parts for callers that keep their experts unquantised, in 8-bit
+ * integers, or train them: products of rows in expert order with each
+ * expert's own matrix, and the movement of rows between token order and
+ * expert order.  Conventions of this section, beside those above:
+ *   - No context, no workspace, no allocation: any number of calls may run at
+ *     once, on any streams of the current device, and all of them can be
+ *     captured into CUDA graphs.  Outputs may not overlap inputs.
+ *   - Matrices are row-major with a contiguous last index.  ld* is a row
+ *     stride in elements, at least the row's length and a multiple of 16
+ *     bytes; matrix pointers are 16-byte aligned, others 4-byte aligned.
+ *     Violations: MOE_ERR_INVALID_ARG.
+ *   - Groups: E experts (1 <= E <= 1024) own the rows offsets[e] ..
+ *     offsets[e + 1] - 1 of P rows (device int32 [E + 1], as moe_route()
+ *     writes them).  A group may be empty.  Output rows outside every group
+ *     are left as they were.  Offsets that fall, are negative or pass P are
+ *     found on the device: nothing is computed.
+ *   - d_status: optional device int32, cleared by the caller, into which the
+ *     kernel ORs 1 (unusable offsets) or 2 (a pipeline wait gave up).
+ *   - Sizes past P <= 2^24 rows or N, K <= 2^20: MOE_ERR_UNSUPPORTED.
+ *   - Sums are held in fp32 (int8 products: exact int32) and rounded once,
+ *     to nearest even, to the output type. */
+
+/* Element types. */
+enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 };
+
+/* moe_route -- the routing arrays of topk_ids (device int32 [T, k]) for the
+ * context's E, k and n_shared, in stream order, into caller buffers (device
+ * int32, laid out as in moe_get_routing(): counts [E + n_shared], offsets
+ * [E + n_shared + 1], perm and inv [T*k + n_shared*T]).  Ids outside [0, E)
+ * drop their slot (inv -1; perm -1 past offsets[E + n_shared]) and raise
+ * MOE_ERR_BAD_ROUTING in the context's device status.  0 <= T <= max_T; with
+ * T = 0 the counts and offsets are zeroed.  The context's own routing record
+ * (moe_get_routing) is not touched; the call uses the context's workspace, so
+ * calls on one context must be stream-ordered. */
+moe_status moe_route(moe_ctx* ctx, int T, const int32_t* topk_ids, int32_t* counts, int32_t* offsets, int32_t* perm,
+                     int32_t* inv, void* stream);
+
+/* moe_permute -- rows into expert order: y[p] = x[t(perm[p])] for 0 <= p <
+ * rows, where slot s stands for token s / k, or, from T*k on, token s - T*k
+ * (the shared expert).  Rows whose slot is -1 or outside are left as they
+ * were.  dtype: MOE_DT_*; x [T, H], y [rows, H], perm device int32 [rows],
+ * 1 <= k <= 32.  Its gradient is moe_combine() with topk_w NULL. */
+moe_status moe_permute(int dtype, int rows, int H, int T, int k, const void* x, long long ldx, const int32_t* perm,
+                       void* y, long long ldy, void* stream);
+
+/* moe_combine -- rows back into token order: out[t] = sum_j topk_w[t, j] *
+ * y[inv[t*k + j]] (+ y[inv[T*k + t]] with n_shared = 1), summed in fp32 in
+ * ascending j, rounded once.  Slots whose inv is -1 or not below rows add
+ * nothing; a token without any gets zeros.  y [rows, H], inv device int32
+ * [T*k + n_shared*T], topk_w device fp32 [T, k] or NULL (ones), out [T, H],
+ * one MOE_DT_* type; 1 <= k <= 32. */
+moe_status moe_combine(int dtype, int rows, int H, int T, int k, int n_shared, const void* y, long long ldy,
+                       const int32_t* inv, const float* topk_w, void* out, long long ldo, void* stream);
+
+/* moe_combine_backward -- gradients of moe_combine(): dy[inv[t*k + j]] =
+ * topk_w[t, j] * dout[t] (the shared expert's rows: dout[t]) and dtopk_w[t, j]
+ * = sum_h dout[t, h] y[inv[t*k + j], h] in fp32, 0 for a dropped slot.  Rows
+ * of dy that no slot names are left as they were.  inv names no row twice
+ * (as moe_route() writes it).  dout [T, H], y and dy [rows, H] of one
+ * MOE_DT_* type, topk_w and dtopk_w device fp32 [T, k]. */
+moe_status moe_combine_backward(int dtype, int rows, int H, int T, int k, int n_shared, const void* dout,
+                                long long lddout, const void* y, long long ldy, const int32_t* inv,
+                                const float* topk_w, void* dy, long long lddy, float* dtopk_w, void* stream);
+
+/* moe_grouped_gemm -- y[p, n] = sum_k x[p, k] w[e, n, k] for every row p of
+ * every group e.  dtype MOE_DT_BF16 or MOE_DT_FP16 (x [P, K] and w), out_dtype
+ * the same or MOE_DT_FP32 (y [P, N]), else MOE_ERR_UNSUPPORTED.  w [E, N, K]
+ * with rows ldw and experts stride_w elements apart (both multiples of 16
+ * bytes; stride_w at least one expert's extent, ignored for E = 1). */
+moe_status moe_grouped_gemm(int dtype, int out_dtype, int E, int P, int N, int K, const int32_t* offsets,
+                            const void* x, long long ldx, const void* w, long long ldw, long long stride_w, void* y,
+                            long long ldy, int32_t* d_status, void* stream);
+
+/* moe_grouped_gemm_dgrad -- the gradient of moe_grouped_gemm() for x: dx[p, k]
+ * = sum_n dy[p, n] w[e, n, k].  dy [P, N] and w of dtype, dx [P, K] of
+ * out_dtype; otherwise as moe_grouped_gemm(). */
+moe_status moe_grouped_gemm_dgrad(int dtype, int out_dtype, int E, int P, int N, int K, const int32_t* offsets,
+                                  const void* dy, long long lddy, const void* w, long long ldw, long long stride_w,
+                                  void* dx, long long lddx, int32_t* d_status, void* stream);
+
+/* moe_grouped_gemm_wgrad -- the gradient for w: dw[e, n, k] = sum over the
+ * rows p of group e of dy[p, n] x[p, k]; zeros for an empty group.  Rows
+ * outside a group take no part in it, whatever they hold.  dy [P, N] and
+ * x [P, K] of dtype, dw [E, N, K] contiguous of out_dtype (K rows a multiple
+ * of 16 bytes), overwritten. */
+moe_status moe_grouped_gemm_wgrad(int dtype, int out_dtype, int E, int P, int N, int K, const int32_t* offsets,
+                                  const void* dy, long long lddy, const void* x, long long ldx, void* dw,
+                                  int32_t* d_status, void* stream);
+
+/* moe_quant_int8 -- rows in 8-bit integers, one scale each: for row p the
+ * token t = t(perm[p]) as in moe_permute() (perm NULL: t = p, rows <= T),
+ * amax = max_k |x[t, k]|, scale[p] = amax / 127 (1 for a row of zeros) and
+ * q[p, k] = rint(127 x[t, k] / amax), ties to even.  A row that holds an
+ * infinity or a NaN gets scale NaN and zeros, so that its products are NaN.
+ * x [T, K] MOE_DT_BF16 or MOE_DT_FP16, q int8 [rows, K], scale device fp32
+ * [rows]; rows whose slot is -1 or outside are left as they were. */
+moe_status moe_quant_int8(int dtype, int rows, int K, int T, int k, const void* x, long long ldx, const int32_t* perm,
+                          int8_t* q, long long ldq, float* scale, void* stream);
+
+/* moe_int8_gemm -- y[p, n] = q_scale[p] w_scale[e, n] sum_k q[p, k] w[e, n, k]:
+ * q int8 [P, K] with one fp32 scale per row (q_scale [P]), w int8 [E, N, K]
+ * with one per output channel (w_scale [E, N] contiguous), exact integer
+ * sums, y [P, N] in any MOE_DT_*.  offsets NULL (E = 1 only): one group of all
+ * rows, the plain dense product.  K <= 131071 (the sums fit 32 bits). */
+moe_status moe_int8_gemm(int out_dtype, int E, int P, int N, int K, const int32_t* offsets, const int8_t* q,
+                         long long ldq, const float* q_scale, const int8_t* w, long long ldw, long long stride_w,
+                         const float* w_scale, void* y, long long ldy, int32_t* d_status, void* stream);
+
 /* moe_status_string -- static description of a status code. */
 const char* moe_status_string(int status);
 
