@@ -7,24 +7,34 @@
 namespace moe {
 namespace {
 
-// One CTA computes tiles of 128 output features by BN rows.  Warp 0 loads
-// both operands with TMA, warp 1 issues the MMAs, warps 4-7 read the
-// accumulators (double-buffered in tensor memory) and store the result.
-template <int KIND, int BN>
+// Tiles of 128 * CG output features by BN rows.  CG = 1: one CTA; CG = 2: a
+// pair of CTAs, each with half of the features and half of the rows' operand
+// in its shared memory.  Warp 0 loads both operands with TMA, warp 1 (of the
+// even CTA) issues the MMAs, warps 4-11 read the accumulators (double-buffered
+// in tensor memory) and store the result.
+template <int KIND, int BN, int CG>
 struct Cfg {
-  static constexpr int THREADS = 256;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int CH = KIND == GG_INT8 ? 128 : 64;  // contraction elements per stage: 128 bytes
+  static constexpr int BR = BN / CG;                     // rows of the tile that this CTA loads
   static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BN * 128;
+  static constexpr int B_BYTES = BR * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TABLE = (2 * (kMaxGroups + 3) + 32) * 4;
   static constexpr int BARS = 512;
-  static constexpr int FIT = (232448 - 1024 - TABLE - BARS) / STAGE;
+  // the epilogue turns CB rows by 32 features per warp and step, through
+  // rows of 64 bytes, 80 apart (no two of eight neighbours share a bank)
+  static constexpr int CB = BN < 32 ? 16 : 32;
+  static constexpr int TURN = EPI_WARPS * CB * 80;
+  static constexpr int FIT = (232448 - 1024 - TABLE - BARS - TURN) / STAGE;
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + TABLE + BARS;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + TABLE + BARS + TURN;
+  static constexpr int BOX = 32;  // rows of a small box (pairs: tiles that are not full)
   static_assert((2 * STAGES + 5) * 8 + 8 <= BARS, "barriers");
-  static_assert(BN % 16 == 0 && BN <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile");
+  static_assert(BN % (16 * CG) == 0 && BN <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile");
+  static_assert(B_BYTES % 1024 == 0, "128-byte swizzle atoms");
 };
 
 // Row tiles of one group are taken in bands of this many, all features of a
@@ -36,10 +46,37 @@ struct Tile {
   int e, m0, p0, rows;
 };
 
-// Tile number u -> group, first feature, first row, rows.  e walks upwards
-// with u, which only grows.
-template <int BN>
-__device__ __forceinline__ Tile tile_of(int u, int NT, const int* s_off, const int* s_tile, int& e) {
+// The tiles as units of work for `teams` CTAs (or pairs): whole tiles while
+// they fill the machine, and the tiles of the last, partial wave cut into
+// 1 << cut pieces by rows when that still is one wave.
+struct Units {
+  int NT, whole, cut, total;
+  template <int BN, int CG>
+  static __device__ __forceinline__ Units make(int tiles, int NT, int teams) {
+    Units w;
+    w.NT = NT;
+    const int rem = tiles % teams;
+    w.whole = tiles - rem;
+    w.cut = 0;
+    if (CG == 2)
+      while (w.cut < 3 && (BN >> (w.cut + 1)) >= 32 && (rem << (w.cut + 1)) <= teams) ++w.cut;
+    w.total = w.whole + (rem << w.cut);
+    return w;
+  }
+};
+
+// Unit u -> group, first feature, first row, rows (none for a piece past the
+// group's end).  e walks upwards with u, which only grows.
+template <int BN, int BM>
+__device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off, const int* s_tile, int& e) {
+  const int NT = w.NT;
+  int piece = 0, width = BN;
+  if (u >= w.whole && w.cut) {
+    const int i = u - w.whole;
+    piece = i & ((1 << w.cut) - 1);
+    u = w.whole + (i >> w.cut);
+    width = BN >> w.cut;
+  }
   const int v = u / NT;
   while (s_tile[e + 1] <= v) ++e;
   const int local = u - s_tile[e] * NT, mt = s_tile[e + 1] - s_tile[e];
@@ -48,32 +85,34 @@ __device__ __forceinline__ Tile tile_of(int u, int NT, const int* s_off, const i
   const int nt = in_band / bw, tt = band * kBand + in_band % bw;
   Tile t;
   t.e = e;
-  t.m0 = nt * 128;
-  t.p0 = s_off[e] + tt * BN;
-  t.rows = min(BN, s_off[e + 1] - t.p0);
+  t.m0 = nt * BM;
+  t.p0 = s_off[e] + tt * BN + piece * width;
+  t.rows = min(width, s_off[e + 1] - t.p0);
   return t;
 }
 
-template <int KIND, int BN>
-__global__ void __launch_bounds__(Cfg<KIND, BN>::THREADS, 1)
+template <int KIND, int BN, int CG>
+__global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const GroupedParams p) {
-  using C = Cfg<KIND, BN>;
+                   const __grid_constant__ CUtensorMap tmXs, const GroupedParams p) {
+  using C = Cfg<KIND, BN, CG>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int* s_off = reinterpret_cast<int*>(smem + STAGES * C::STAGE);
   int* s_tile = s_off + kMaxGroups + 3;
   int* s_scan = s_tile + kMaxGroups + 3;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE + C::TABLE);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE + C::TABLE);  // (even CTA's are used)
+  uint64_t* empty = full + STAGES;   // a commit to each CTA
+  uint64_t* tfull = empty + STAGES;  // a commit to each CTA
+  uint64_t* tempty = tfull + 2;      // (even CTA) the epilogue warps of each CTA
   uint64_t* done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int team = blockIdx.x / CG, teams = gridDim.x / CG;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -81,35 +120,42 @@ __global__ void __launch_bounds__(Cfg<KIND, BN>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], C::EPI_WARPS * CG);
     }
     mbar_init(done, 1);
     *abort = 0;
     mbar_fence_init();
     tma_prefetch_map(&tmW);
     tma_prefetch_map(&tmX);
+    if (CG == 2) tma_prefetch_map(&tmXs);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, C::TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_holder, C::TMEM_COLS);
   tc_fence_before();
   const bool good = build_group_table<C::THREADS>(p.offsets, p.E, p.P, BN, s_off, s_tile, s_scan);
+  if (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any signal crosses
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int NT = (p.M + 127) / 128;
-  const int total = good ? s_tile[p.E] * NT : 0;
+  const int NT = (p.M + 128 * CG - 1) / (128 * CG);
+  const Units work = Units::make<BN, CG>(good ? s_tile[p.E] * NT : 0, NT, teams);
   const int KB = (p.R + C::CH - 1) / C::CH;
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol_w = p.stream_w ? policy_evict_first() : policy_evict_normal();
       const uint64_t pol_x = policy_evict_normal();
+      const uint32_t full0 = CG == 2 ? mapa_rank(full, 0) : smem_u32(full);
       uint32_t armed = 0, parity = 0;
       bool ok = true;
       int it = 0, e = 0;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Tile t = tile_of<BN>(u, NT, s_off, s_tile, e);
+      for (int u = team; u < work.total && ok; u += teams) {
+        const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+        if (t.rows <= 0) continue;
+        // the MMA covers the tile's rows rounded up; each CTA of a pair
+        // holds half of them, in small boxes unless the tile is full
+        const int n = CG == 2 ? (t.rows + 31) & ~31 : BN;
+        const int boxes = CG == 1 || n == BN ? 0 : (n / 2 + C::BOX - 1) / C::BOX;
+        const uint32_t bytes = CG == 1 || n == BN ? CG * C::STAGE : 2 * (C::A_BYTES + boxes * C::BOX * 128);
+        const int m0 = t.m0 + (int)rank * 128, p0 = t.p0 + (int)rank * (n / CG);
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int st = it % STAGES;
           const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
@@ -117,31 +163,51 @@ __global__ void __launch_bounds__(Cfg<KIND, BN>::THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[st], C::STAGE);
+          // the even CTA posts the bytes of both
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
           armed |= 1u << st;
           parity = (parity & ~(1u << st)) | (ph << st);
           uint8_t* a = smem + st * C::STAGE;
-          if (KIND == GG_DGRAD) {
-            tma_load_3d(&tmW, &full[st], a, t.m0, kb * C::CH, t.e, pol_w);
-            tma_load_3d(&tmW, &full[st], a + C::A_BYTES / 2, t.m0 + 64, kb * C::CH, t.e, pol_w);
+          const int r0 = kb * C::CH;
+          if constexpr (CG == 1) {
+            if (KIND == GG_DGRAD) {
+              tma_load_3d(&tmW, &full[st], a, m0, r0, t.e, pol_w);
+              tma_load_3d(&tmW, &full[st], a + C::A_BYTES / 2, m0 + 64, r0, t.e, pol_w);
+            } else {
+              tma_load_3d(&tmW, &full[st], a, r0, m0, t.e, pol_w);
+            }
+            tma_load_2d(&tmX, &full[st], a + C::A_BYTES, r0, p0, pol_x);
           } else {
-            tma_load_3d(&tmW, &full[st], a, kb * C::CH, t.m0, t.e, pol_w);
+            const uint32_t bar = full0 + 8u * st;
+            if (KIND == GG_DGRAD) {
+              tma_load_3d_pair(&tmW, bar, a, m0, r0, t.e, pol_w);
+              tma_load_3d_pair(&tmW, bar, a + C::A_BYTES / 2, m0 + 64, r0, t.e, pol_w);
+            } else {
+              tma_load_3d_pair(&tmW, bar, a, r0, m0, t.e, pol_w);
+            }
+            if (boxes == 0) tma_load_2d_pair(&tmX, bar, a + C::A_BYTES, r0, p0, pol_x);
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(&tmXs, bar, a + C::A_BYTES + b * C::BOX * 128, r0, p0 + b * C::BOX, pol_x);
           }
-          tma_load_2d(&tmX, &full[st], a + C::A_BYTES, kb * C::CH, t.p0, pol_x);
         }
       }
-      // after an abort: every copy in flight lands before the CTA leaves
-      if (*abort)
+      // after an abort: the copies in flight land before the CTAs leave (the
+      // even CTA's barriers count both CTAs' bytes)
+      if (*abort && rank == 0)
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s)) mbar_drain(&full[s], (parity >> s) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = p.idesc;
+    if (lane == 0 && rank == 0) {
+      const uint32_t empty1 = CG == 2 ? mapa_rank(empty, 1) : 0, tfull1 = CG == 2 ? mapa_rank(tfull, 1) : 0;
       bool ok = true;
-      int it = 0, j = 0;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++j) {
+      int it = 0, j = 0, e = 0;
+      for (int u = team; u < work.total && ok; u += teams) {
+        const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+        if (t.rows <= 0) continue;
+        const int n = (t.rows + 16 * CG - 1) & ~(16 * CG - 1);
+        const uint32_t idesc = p.idesc | (uint32_t)(n >> 3) << 17;
         const int buf = j & 1;
         ok = mbar_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
         if (!ok) break;
@@ -161,101 +227,188 @@ __global__ void __launch_bounds__(Cfg<KIND, BN>::THREADS, 1)
             // 32 bytes of the contraction per instruction, or 16 rows of 128 bytes
             const uint64_t da = ad + (KIND == GG_DGRAD ? 128 * kk : 2 * kk);
             if (KIND == GG_INT8)
-              mma_s8(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
+              mma_s8<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
             else
-              mma_f16(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
+              mma_f16<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
           }
-          mma_commit(&empty[st]);
+          mma_commit_at<CG>(smem_u32(&empty[st]));
+          if (CG == 2) mma_commit_at<CG>(empty1 + 8u * st);
         }
-        if (ok) mma_commit(&tfull[buf]);
+        if (ok) {
+          mma_commit_at<CG>(smem_u32(&tfull[buf]));
+          if (CG == 2) mma_commit_at<CG>(tfull1 + 8u * buf);
+        }
+        ++j;
       }
-      mma_commit(done);
+      mma_commit_at<CG>(smem_u32(done));
       mbar_drain(done, 0);
     }
     __syncwarp();
   } else if (warp >= 4) {
-    const int q = warp & 3;
+    // Two warps per quarter of the features share the tile's rows, CB by CB.
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tempty0 = CG == 2 ? mapa_rank(tempty, 0) : smem_u32(tempty);
+    uint8_t* turn = smem + STAGES * C::STAGE + C::TABLE + C::BARS + (warp - 4) * C::CB * 80;
+    const uint32_t turn_st = smem_u32(turn) + (lane & 7) * 80 + (lane >> 3) * 16;
     bool ok = true;
     int j = 0, e = 0;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++j) {
-      const Tile t = tile_of<BN>(u, NT, s_off, s_tile, e);
+    for (int u = team; u < work.total && ok; u += teams) {
+      const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+      if (t.rows <= 0) continue;
       const int buf = j & 1;
+      const int m0 = t.m0 + (int)rank * 128 + q * 32;  // this warp's first feature
+      // int8: the scales of the features this thread holds
+      float cs[4];
+      if (KIND == GG_INT8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = p.out_type == MOE_DT_FP32 ? m0 + lane : m0 + i * 8 + (lane >> 2);
+          cs[i] = m < p.M ? __ldg(p.col_scale + (size_t)t.e * p.M + m) : 0.0f;
+        }
+      }
       ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      const int m = t.m0 + q * 32 + lane;
-      const bool in = m < p.M;
-      const float cs = (KIND == GG_INT8 && in) ? p.col_scale[(size_t)t.e * p.M + m] : 1.0f;
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
+      for (int c0 = half * C::CB; c0 < t.rows && m0 < p.M; c0 += 2 * C::CB) {
+        const int left = t.rows - c0;  // rows of this step: min(left, CB)
+        if (p.out_type == MOE_DT_FP32) {
+          // a lane is a feature, a register a row: 128 contiguous bytes per store
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 16) {
-        if (c0 >= t.rows) break;
-        float v[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * BN + c0, v);
-        tmem_wait_ld();
+          for (int h = 0; h < C::CB && h < left; h += 16) {
+            float v[16];
+            tmem_ld16(acc + c0 + h, v);
+            tmem_wait_ld();
+            float* y = static_cast<float*>(p.y) + (size_t)(t.p0 + c0 + h) * p.ldy + m0 + lane;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (c0 + c < t.rows && in) {
-            const size_t row = (size_t)(t.p0 + c0 + c);
-            float r = v[c];
-            if (KIND == GG_INT8) r = __fmul_rn(__fmul_rn((float)__float_as_int(r), p.row_scale[row]), cs);
-            const size_t at = row * p.ldy + m;
-            if (p.out_type == MOE_DT_FP32) static_cast<float*>(p.y)[at] = r;
-            else if (p.out_type == MOE_DT_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(r);
-            else static_cast<__half*>(p.y)[at] = __float2half_rn(r);
+            for (int c = 0; c < 16; ++c) {
+              if (h + c >= left || m0 + lane >= p.M) continue;
+              float r = v[c];
+              if (KIND == GG_INT8)
+                r = __fmul_rn(__fmul_rn((float)__float_as_int(r), __ldg(p.row_scale + t.p0 + c0 + h + c)), cs[0]);
+              y[c * p.ldy] = r;
+            }
+          }
+          continue;
+        }
+        constexpr int NG = C::CB / 8;
+        uint32_t f[2][NG * 4];
+        tmem_ld_16x256b<NG>(acc + c0, f[0]);
+        tmem_ld_16x256b<NG>(acc + (16u << 16) + c0, f[1]);
+        tmem_wait_ld();
+        const bool bf = p.out_type == MOE_DT_BF16;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          uint32_t w[4];
+          float rs[2];
+          if (KIND == GG_INT8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = i * 8 + (lane & 3) * 2 + h;
+              rs[h] = c < left ? __ldg(p.row_scale + t.p0 + c0 + c) : 0.0f;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {  // features 8 g .. 8 g + 7 of the warp's 32
+            float a = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2]);
+            float b = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2 + 1]);
+            if (KIND == GG_INT8) {
+              a = __fmul_rn(__fmul_rn((float)__float_as_int(a), rs[0]), cs[g]);
+              b = __fmul_rn(__fmul_rn((float)__float_as_int(b), rs[1]), cs[g]);
+            }
+            w[g] = pack16(a, b, bf);
+          }
+          stmatrix_x4_trans(turn_st + i * 8 * 80, w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(t.p0 + c0) * p.ldy + m0;
+#pragma unroll
+        for (int i = 0; i < C::CB / 8; ++i) {
+          const int c = i * 8 + (lane >> 2), part = (lane & 3) * 8;
+          if (c < left && m0 + part < p.M) {
+            const uint4 v = *reinterpret_cast<const uint4*>(turn + c * 80 + part * 2);
+            uint16_t* to = y + c * p.ldy + part;
+            if (m0 + part + 8 <= p.M) {
+              *reinterpret_cast<uint4*>(to) = v;
+            } else {
+              const uint16_t* x = reinterpret_cast<const uint16_t*>(&v);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (m0 + part + k < p.M) to[k] = x[k];
+            }
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
+      ++j;
     }
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA leaves while the other may still signal it or read its memory
+  if (CG == 2) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) tmem_dealloc_cg<CG>(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && p.status) {
     if (*abort) atomicOr(p.status, DEV_TIMEOUT);
     if (!good) atomicOr(p.status, DEV_BAD_ROUTING);
   }
 }
 
-template <int KIND, int BN>
-cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const GroupedParams& p, int grid, cudaStream_t s) {
-  using C = Cfg<KIND, BN>;
+template <int KIND, int BN, int CG>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs, const GroupedParams& p, int sms, cudaStream_t s) {
+  using C = Cfg<KIND, BN, CG>;
   // per device: the attribute belongs to the current device's context
-  const cudaError_t e = cudaFuncSetAttribute(grouped_kernel<KIND, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t e =
+      cudaFuncSetAttribute(grouped_kernel<KIND, BN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  grouped_kernel<KIND, BN><<<grid, C::THREADS, C::SMEM, s>>>(tw, tx, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / CG * CG);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<KIND, BN, CG>, tw, tx, txs, p);
 }
 
 }  // namespace
 
-int grouped_tile_rows(const GroupedParams& p) {
+GroupedTile grouped_tile(const GroupedParams& p) {
   const long long avg = ((long long)p.P + p.E - 1) / p.E;
-  return avg <= 16 ? 16 : avg <= 64 ? 64 : 256;
+  if (avg <= 16) return {16, 1};
+  if (avg <= 64) return {64, 1};
+  return {256, 2};
 }
 
 template <int KIND>
-static cudaError_t launch_kind(int bn, const CUtensorMap& tw, const CUtensorMap& tx, const GroupedParams& p, int grid,
-                               cudaStream_t s) {
-  switch (bn) {
-    case 16: return launch<KIND, 16>(tw, tx, p, grid, s);
-    case 64: return launch<KIND, 64>(tw, tx, p, grid, s);
-    case 256: return launch<KIND, 256>(tw, tx, p, grid, s);
+static cudaError_t launch_kind(GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs,
+                               const GroupedParams& p, int sms, cudaStream_t s) {
+  switch (t.rows) {
+    case 16: return launch<KIND, 16, 1>(tw, tx, txs, p, sms, s);
+    case 64: return launch<KIND, 64, 1>(tw, tx, txs, p, sms, s);
+    case 256: return launch<KIND, 256, 2>(tw, tx, txs, p, sms, s);
   }
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_grouped(int kind, int bn, const CUtensorMap& tw, const CUtensorMap& tx, const GroupedParams& p0,
-                           int sms, cudaStream_t s) {
+cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,
+                           const CUtensorMap& txs, const GroupedParams& p0, int sms, cudaStream_t s) {
   GroupedParams p = p0;
-  p.idesc = kind == GG_INT8 ? idesc_s8(128, bn) : idesc_f16(128, bn, p.fmt, kind == GG_DGRAD, 0);
-  if (kind == GG_FWD) return launch_kind<GG_FWD>(bn, tw, tx, p, sms, s);
-  if (kind == GG_DGRAD) return launch_kind<GG_DGRAD>(bn, tw, tx, p, sms, s);
-  return launch_kind<GG_INT8>(bn, tw, tx, p, sms, s);
+  // N is set tile by tile
+  p.idesc = kind == GG_INT8 ? idesc_s8(128 * t.ctas, 0) : idesc_f16(128 * t.ctas, 0, p.fmt, kind == GG_DGRAD, 0);
+  if (kind == GG_FWD) return launch_kind<GG_FWD>(t, tw, tx, txs, p, sms, s);
+  if (kind == GG_DGRAD) return launch_kind<GG_DGRAD>(t, tw, tx, txs, p, sms, s);
+  return launch_kind<GG_INT8>(t, tw, tx, txs, p, sms, s);
 }
 
 }  // namespace moe

@@ -87,10 +87,14 @@ struct RowCombineBwdParams {
   float* dg;                // [T, k]
 };
 
-// Rows of one tile (the rows side of the MMA) for this call's rows and groups.
-int grouped_tile_rows(const GroupedParams& p);
-cudaError_t launch_grouped(int kind, int bn, const CUtensorMap& tw, const CUtensorMap& tx, const GroupedParams& p,
-                           int sms, cudaStream_t s);
+// How a call is tiled: rows of one tile (the rows side of the MMA), and CTAs
+// that work on a tile together.  tx has boxes of rows / ctas rows, txs of 32.
+struct GroupedTile {
+  int rows, ctas;
+};
+GroupedTile grouped_tile(const GroupedParams& p);
+cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,
+                           const CUtensorMap& txs, const GroupedParams& p, int sms, cudaStream_t s);
 cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const WgradParams& p, int sms, cudaStream_t s);
 cudaError_t launch_quant_int8(const QuantInt8Params& p, int dtype, cudaStream_t s);
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
           const uint64_t ad = sdesc_mn_sw128(smem_u32(a), C::BOX);
           const uint64_t bd = sdesc_mn_sw128(smem_u32(a + C::NA * C::BOX), C::BOX);
           for (int kk = 0; kk < steps; ++kk)
-            mma_f16(tmem + buf * C::BN, ad + 128 * kk, bd + 128 * kk, p.idesc, (row != lo) | (kk != 0));
+            mma_f16<1>(tmem + buf * C::BN, ad + 128 * kk, bd + 128 * kk, p.idesc, (row != lo) | (kk != 0));
           mma_commit(&empty[st]);
         }
         __syncwarp();
