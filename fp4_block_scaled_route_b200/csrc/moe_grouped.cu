@@ -9,10 +9,11 @@ namespace {
 
 // Tiles of 128 * CG output features by BN rows.  CG = 1: one CTA; CG = 2: a
 // pair of CTAs, each with half of the features and half of the rows' operand
-// in its shared memory.  Warp 0 loads both operands with TMA, warp 1 (of the
+// in its shared memory.  SPLIT (CG = 1): the CTAs of a cluster share a tile's
+// contraction, and the first joins their partial sums.  Warp 0 loads both operands with TMA, warp 1 (of the
 // even CTA) issues the MMAs, warps 4-11 read the accumulators (double-buffered
 // in tensor memory) and store the result.
-template <int KIND, int BN, int CG>
+template <int KIND, int BN, int CG, bool SPLIT>
 struct Cfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
@@ -25,15 +26,19 @@ struct Cfg {
   static constexpr int BARS = 512;
   // the epilogue turns CB rows by 32 features per warp and step, through
   // rows of 64 bytes, 80 apart (no two of eight neighbours share a bank)
-  static constexpr int CB = BN < 32 ? 16 : 32;
+  static constexpr int CB = BN <= 32 ? 16 : 32;
   static constexpr int TURN = EPI_WARPS * CB * 80;
-  static constexpr int FIT = (232448 - 1024 - TABLE - BARS - TURN) / STAGE;
+  // SPLIT: the partial sums of up to MAX_SPLIT - 1 other CTAs
+  static constexpr int MAX_SPLIT = !SPLIT ? 1 : BN <= 32 ? 8 : 4;
+  static constexpr int JOIN = (MAX_SPLIT - 1) * 128 * BN * 4;
+  static constexpr int FIT = (232448 - 1024 - TABLE - BARS - TURN - JOIN) / STAGE;
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + TABLE + BARS + TURN;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + TABLE + BARS + TURN + JOIN;
   static constexpr int BOX = 32;  // rows of a small box (pairs: tiles that are not full)
-  static_assert((2 * STAGES + 5) * 8 + 8 <= BARS, "barriers");
+  static_assert((2 * STAGES + 6) * 8 + 8 <= BARS, "barriers");
   static_assert(BN % (16 * CG) == 0 && BN <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile");
+  static_assert(!SPLIT || CG == 1, "clusters either pair up or share a contraction");
   static_assert(B_BYTES % 1024 == 0, "128-byte swizzle atoms");
 };
 
@@ -42,9 +47,18 @@ struct Cfg {
 // rows and their weights in the L2.
 constexpr int kBand = 8;
 
+// Contraction steps (128 bytes each) that a share of a split tile keeps.
+constexpr int kMinChunks = 4;
+
 struct Tile {
   int e, m0, p0, rows;
 };
+
+template <int KIND>
+__device__ __forceinline__ uint32_t add_as(uint32_t a, uint32_t b) {
+  if (KIND == GG_INT8) return a + b;
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
 
 // The tiles as units of work for `teams` CTAs (or pairs): whole tiles while
 // they fill the machine, and the tiles of the last, partial wave cut into
@@ -91,11 +105,11 @@ __device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off,
   return t;
 }
 
-template <int KIND, int BN, int CG>
-__global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
+template <int KIND, int BN, int CG, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmXs, const GroupedParams p) {
-  using C = Cfg<KIND, BN, CG>;
+  using C = Cfg<KIND, BN, CG, SPLIT>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -106,13 +120,15 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
   uint64_t* empty = full + STAGES;   // a commit to each CTA
   uint64_t* tfull = empty + STAGES;  // a commit to each CTA
   uint64_t* tempty = tfull + 2;      // (even CTA) the epilogue warps of each CTA
-  uint64_t* done = tempty + 2;
+  uint64_t* joined = tempty + 2;     // (SPLIT, first CTA) the other CTAs' epilogue warps
+  uint64_t* done = joined + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const int team = blockIdx.x / CG, teams = gridDim.x / CG;
+  const uint32_t rank = CG == 2 || SPLIT ? cluster_rank() : 0;
+  const int split = SPLIT ? p.split : 1, size = CG * split;  // CTAs that work on a tile
+  const int team = blockIdx.x / size, teams = gridDim.x / size;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -122,6 +138,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], C::EPI_WARPS * CG);
     }
+    if (SPLIT) mbar_init(joined, (split - 1) * C::EPI_WARPS);
     mbar_init(done, 1);
     *abort = 0;
     mbar_fence_init();
@@ -130,14 +147,21 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
     if (CG == 2) tma_prefetch_map(&tmXs);
   }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_holder, C::TMEM_COLS);
+  // everything above ran while the kernel before this one could still be
+  // running; nothing of its results is read before this point
+  griddep_wait();
   tc_fence_before();
   const bool good = build_group_table<C::THREADS>(p.offsets, p.E, p.P, BN, s_off, s_tile, s_scan);
-  if (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any signal crosses
+  if (CG == 2 || SPLIT) cluster_sync_all();  // the CTAs' barriers exist before any signal crosses
   tc_fence_after();
+  griddep_launch_dependents();  // (tensor memory is held: no later kernel can take it first)
   const uint32_t tmem = *tmem_holder;
   const int NT = (p.M + 128 * CG - 1) / (128 * CG);
   const Units work = Units::make<BN, CG>(good ? s_tile[p.E] * NT : 0, NT, teams);
-  const int KB = (p.R + C::CH - 1) / C::CH;
+  const int chunks = (p.R + C::CH - 1) / C::CH;
+  // this CTA's part of the contraction
+  const int kb0 = SPLIT ? (int)((long long)chunks * rank / split) : 0;
+  const int kb1 = SPLIT ? (int)((long long)chunks * (rank + 1) / split) : chunks;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -155,8 +179,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
         const int n = CG == 2 ? (t.rows + 31) & ~31 : BN;
         const int boxes = CG == 1 || n == BN ? 0 : (n / 2 + C::BOX - 1) / C::BOX;
         const uint32_t bytes = CG == 1 || n == BN ? CG * C::STAGE : 2 * (C::A_BYTES + boxes * C::BOX * 128);
-        const int m0 = t.m0 + (int)rank * 128, p0 = t.p0 + (int)rank * (n / CG);
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int half = CG == 2 ? (int)rank : 0;
+        const int m0 = t.m0 + half * 128, p0 = t.p0 + half * (n / CG);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int st = it % STAGES;
           const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
           if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
@@ -164,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
             break;
           }
           // the even CTA posts the bytes of both
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
           armed |= 1u << st;
           parity = (parity & ~(1u << st)) | (ph << st);
           uint8_t* a = smem + st * C::STAGE;
@@ -193,13 +218,13 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
       }
       // after an abort: the copies in flight land before the CTAs leave (the
       // even CTA's barriers count both CTAs' bytes)
-      if (*abort && rank == 0)
+      if (*abort && (CG == 1 || rank == 0))
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s)) mbar_drain(&full[s], (parity >> s) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (lane == 0 && (CG == 1 || rank == 0)) {
       const uint32_t empty1 = CG == 2 ? mapa_rank(empty, 1) : 0, tfull1 = CG == 2 ? mapa_rank(tfull, 1) : 0;
       bool ok = true;
       int it = 0, j = 0, e = 0;
@@ -212,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
         ok = mbar_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
         if (!ok) break;
         tc_fence_after();
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int st = it % STAGES;
           if (!mbar_wait(&full[st], (uint32_t)(it / STAGES) & 1u, abort)) {
             ok = false;
@@ -227,9 +252,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
             // 32 bytes of the contraction per instruction, or 16 rows of 128 bytes
             const uint64_t da = ad + (KIND == GG_DGRAD ? 128 * kk : 2 * kk);
             if (KIND == GG_INT8)
-              mma_s8<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
+              mma_s8<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb != kb0) | (kk != 0));
             else
-              mma_f16<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb | kk) != 0);
+              mma_f16<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb != kb0) | (kk != 0));
           }
           mma_commit_at<CG>(smem_u32(&empty[st]));
           if (CG == 2) mma_commit_at<CG>(empty1 + 8u * st);
@@ -248,6 +273,11 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
     // Two warps per quarter of the features share the tile's rows, CB by CB.
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tempty0 = CG == 2 ? mapa_rank(tempty, 0) : smem_u32(tempty);
+    // SPLIT: [other CTA][warp][step][register / 4][lane][4] words
+    constexpr int STEPS = (BN + 2 * C::CB - 1) / (2 * C::CB), NG = C::CB / 8;
+    uint32_t* join = reinterpret_cast<uint32_t*>(smem + STAGES * C::STAGE + C::TABLE + C::BARS + C::TURN);
+    constexpr int PER_WARP = STEPS * NG * 8 * 32, PER_CTA = 128 * BN;
+    static_assert((BN < 2 * C::CB ? 4 : 8) * PER_WARP == PER_CTA, "partial sums");
     uint8_t* turn = smem + STAGES * C::STAGE + C::TABLE + C::BARS + (warp - 4) * C::CB * 80;
     const uint32_t turn_st = smem_u32(turn) + (lane & 7) * 80 + (lane >> 3) * 16;
     bool ok = true;
@@ -256,13 +286,13 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       if (t.rows <= 0) continue;
       const int buf = j & 1;
-      const int m0 = t.m0 + (int)rank * 128 + q * 32;  // this warp's first feature
+      const int m0 = t.m0 + (CG == 2 ? (int)rank * 128 : 0) + q * 32;  // this warp's first feature
       // int8: the scales of the features this thread holds
       float cs[4];
       if (KIND == GG_INT8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int m = p.out_type == MOE_DT_FP32 ? m0 + lane : m0 + i * 8 + (lane >> 2);
+          const int m = m0 + i * 8 + (lane >> 2);
           cs[i] = m < p.M ? __ldg(p.col_scale + (size_t)t.e * p.M + m) : 0.0f;
         }
       }
@@ -271,32 +301,42 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
+      // the other CTAs' sums have arrived (data written by them: acquire)
+      if (SPLIT && rank == 0) {
+        ok = mbar_wait_cluster(joined, 0, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+      }
       for (int c0 = half * C::CB; c0 < t.rows && m0 < p.M; c0 += 2 * C::CB) {
         const int left = t.rows - c0;  // rows of this step: min(left, CB)
-        if (p.out_type == MOE_DT_FP32) {
-          // a lane is a feature, a register a row: 128 contiguous bytes per store
-#pragma unroll 1
-          for (int h = 0; h < C::CB && h < left; h += 16) {
-            float v[16];
-            tmem_ld16(acc + c0 + h, v);
-            tmem_wait_ld();
-            float* y = static_cast<float*>(p.y) + (size_t)(t.p0 + c0 + h) * p.ldy + m0 + lane;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (h + c >= left || m0 + lane >= p.M) continue;
-              float r = v[c];
-              if (KIND == GG_INT8)
-                r = __fmul_rn(__fmul_rn((float)__float_as_int(r), __ldg(p.row_scale + t.p0 + c0 + h + c)), cs[0]);
-              y[c * p.ldy] = r;
-            }
-          }
-          continue;
-        }
-        constexpr int NG = C::CB / 8;
         uint32_t f[2][NG * 4];
         tmem_ld_16x256b<NG>(acc + c0, f[0]);
         tmem_ld_16x256b<NG>(acc + (16u << 16) + c0, f[1]);
         tmem_wait_ld();
+        if (SPLIT) {
+          uint32_t* at = join + (warp - 4) * PER_WARP + (c0 / (2 * C::CB)) * (NG * 8 * 32) + lane * 4;
+          if (rank != 0) {
+            const uint32_t to = mapa_rank(at + (rank - 1) * PER_CTA, 0);
+#pragma unroll
+            for (int i = 0; i < NG * 2; ++i) {
+              const uint32_t* v = &f[i / NG][(i % NG) * 4];
+              st_cluster_v4(to + i * 512, v[0], v[1], v[2], v[3]);
+            }
+            continue;
+          }
+          // in the CTAs' order, whatever order they finished in
+          for (int r = 0; r < split - 1; ++r) {
+#pragma unroll
+            for (int i = 0; i < NG * 2; ++i) {
+              const uint4 o = *reinterpret_cast<const uint4*>(at + r * PER_CTA + i * 128);
+              uint32_t* v = &f[i / NG][(i % NG) * 4];
+              v[0] = add_as<KIND>(v[0], o.x);
+              v[1] = add_as<KIND>(v[1], o.y);
+              v[2] = add_as<KIND>(v[2], o.z);
+              v[3] = add_as<KIND>(v[3], o.w);
+            }
+          }
+        }
         const bool bf = p.out_type == MOE_DT_BF16;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -317,10 +357,20 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
               a = __fmul_rn(__fmul_rn((float)__float_as_int(a), rs[0]), cs[g]);
               b = __fmul_rn(__fmul_rn((float)__float_as_int(b), rs[1]), cs[g]);
             }
-            w[g] = pack16(a, b, bf);
+            if (p.out_type == MOE_DT_FP32) {
+              // eight neighbouring lanes (l / 4) fill a 32-byte sector of one row
+              const int m = m0 + g * 8 + (lane >> 2), c = i * 8 + (lane & 3) * 2;
+              float* y = static_cast<float*>(p.y) + (size_t)(t.p0 + c0 + c) * p.ldy + m;
+              if (m < p.M && c < left) y[0] = a;
+              if (m < p.M && c + 1 < left) y[p.ldy] = b;
+            } else {
+              w[g] = pack16(a, b, bf);
+            }
           }
+          if (p.out_type == MOE_DT_FP32) continue;
           stmatrix_x4_trans(turn_st + i * 8 * 80, w[0], w[1], w[2], w[3]);
         }
+        if (p.out_type == MOE_DT_FP32) continue;
         __syncwarp();
         uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(t.p0 + c0) * p.ldy + m0;
 #pragma unroll
@@ -343,14 +393,15 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
+      if (SPLIT && rank != 0 && lane == 0) mbar_arrive_at(mapa_rank(joined, 0));
       if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
       ++j;
     }
   }
   tc_fence_before();
   __syncthreads();
-  // neither CTA leaves while the other may still signal it or read its memory
-  if (CG == 2) cluster_sync_all();
+  // no CTA of a cluster leaves while another may still signal it or use its memory
+  if (CG == 2 || SPLIT) cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_cg<CG>(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && p.status) {
@@ -359,56 +410,66 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG>::THREADS, 1)
   }
 }
 
-template <int KIND, int BN, int CG>
-cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs, const GroupedParams& p, int sms, cudaStream_t s) {
-  using C = Cfg<KIND, BN, CG>;
-  // per device: the attribute belongs to the current device's context
-  const cudaError_t e =
-      cudaFuncSetAttribute(grouped_kernel<KIND, BN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms / CG * CG);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, grouped_kernel<KIND, BN, CG>, tw, tx, txs, p);
+template <int KIND, int BN, int CG, bool SPLIT>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs, const GroupedParams& p,
+                   int grid, cudaStream_t s) {
+  using C = Cfg<KIND, BN, CG, SPLIT>;
+  if (SPLIT && p.split > C::MAX_SPLIT) return cudaErrorInvalidValue;
+  return launch_cluster(grouped_kernel<KIND, BN, CG, SPLIT>, grid, C::THREADS, C::SMEM, SPLIT ? p.split : CG, s, tw, tx,
+                        txs, p);
 }
 
 }  // namespace
 
-GroupedTile grouped_tile(const GroupedParams& p) {
-  const long long avg = ((long long)p.P + p.E - 1) / p.E;
-  if (avg <= 16) return {16, 1};
-  if (avg <= 64) return {64, 1};
-  return {256, 2};
+GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
+  // Rows a tile should hold: the group's when there is one, else twice the
+  // average, since routed groups vary.
+  const long long want = p.E == 1 ? p.P : 2LL * ((p.P + p.E - 1) / p.E);
+  GroupedTile t{want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 256, 1, 1, sms};
+  if (t.rows == 256) {
+    t.ctas = 2;
+    t.grid = sms / 2 * 2;
+    return t;
+  }
+  // Few tiles (at most one per group with rows, and one per full tile): share
+  // the contraction while every share keeps kMinChunks steps and all CTAs
+  // are resident at once; each cluster then takes one tile.
+  const int chunks = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
+  const long long most = ((p.E < p.P ? p.E : p.P) + p.P / t.rows) * (long long)((p.M + 127) / 128);
+  const int limit = t.rows <= 32 ? 8 : 4;
+  while (t.split < limit && most * t.split * 2 <= sms && chunks >= t.split * 2 * kMinChunks) t.split *= 2;
+  if (t.split > 1) t.grid = (int)most * t.split;
+  return t;
 }
 
 template <int KIND>
 static cudaError_t launch_kind(GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs,
-                               const GroupedParams& p, int sms, cudaStream_t s) {
+                               const GroupedParams& p, cudaStream_t s) {
+  const bool split = t.split > 1;
   switch (t.rows) {
-    case 16: return launch<KIND, 16, 1>(tw, tx, txs, p, sms, s);
-    case 64: return launch<KIND, 64, 1>(tw, tx, txs, p, sms, s);
-    case 256: return launch<KIND, 256, 2>(tw, tx, txs, p, sms, s);
+    case 16:
+      return split ? launch<KIND, 16, 1, true>(tw, tx, txs, p, t.grid, s)
+                   : launch<KIND, 16, 1, false>(tw, tx, txs, p, t.grid, s);
+    case 32:
+      return split ? launch<KIND, 32, 1, true>(tw, tx, txs, p, t.grid, s)
+                   : launch<KIND, 32, 1, false>(tw, tx, txs, p, t.grid, s);
+    case 64:
+      return split ? launch<KIND, 64, 1, true>(tw, tx, txs, p, t.grid, s)
+                   : launch<KIND, 64, 1, false>(tw, tx, txs, p, t.grid, s);
+    case 256: return launch<KIND, 256, 2, false>(tw, tx, txs, p, t.grid, s);
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,
-                           const CUtensorMap& txs, const GroupedParams& p0, int sms, cudaStream_t s) {
+                           const CUtensorMap& txs, const GroupedParams& p0, cudaStream_t s) {
   GroupedParams p = p0;
+  p.split = t.split;
   // N is set tile by tile
   p.idesc = kind == GG_INT8 ? idesc_s8(128 * t.ctas, 0) : idesc_f16(128 * t.ctas, 0, p.fmt, kind == GG_DGRAD, 0);
-  if (kind == GG_FWD) return launch_kind<GG_FWD>(t, tw, tx, txs, p, sms, s);
-  if (kind == GG_DGRAD) return launch_kind<GG_DGRAD>(t, tw, tx, txs, p, sms, s);
-  return launch_kind<GG_INT8>(t, tw, tx, txs, p, sms, s);
+  if (kind == GG_FWD) return launch_kind<GG_FWD>(t, tw, tx, txs, p, s);
+  if (kind == GG_DGRAD) return launch_kind<GG_DGRAD>(t, tw, tx, txs, p, s);
+  return launch_kind<GG_INT8>(t, tw, tx, txs, p, s);
 }
 
 }  // namespace moe

@@ -114,15 +114,15 @@ moe_status run_grouped(int kind, int dtype, int out_dtype, int E, int P, int N, 
   p.fmt = dtype == MOE_DT_BF16 ? 1 : 0;
   p.row_scale = row_scale; p.col_scale = col_scale;
   p.status = d_status;
-  const moe::GroupedTile t = moe::grouped_tile(p);
+  const moe::GroupedTile t = moe::grouped_tile(p, kind, sms);
   p.stream_w = t.rows < 256;
-  CUtensorMap tw, tx, txs;
+  CUtensorMap tw, tx, txs{};
   const CUtensorMapDataType dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(dtype);
   if (!make_map(&tw, dt, es, w, K, N, ldw, E, E > 1 ? stride_w : (long long)N * ldw, kind == moe::GG_DGRAD ? 64 : 128) ||
       !make_map(&tx, dt, es, x, R, P, ldx, 0, 0, t.rows / t.ctas) ||
-      !make_map(&txs, dt, es, x, R, P, ldx, 0, 0, 32))
+      (t.ctas > 1 && !make_map(&txs, dt, es, x, R, P, ldx, 0, 0, 32)))
     return MOE_ERR_CUDA;
-  return moe::launch_grouped(kind, t, tw, tx, txs, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+  return moe::launch_grouped(kind, t, tw, tx, txs, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
                                                                                                       : MOE_ERR_CUDA;
 }
 

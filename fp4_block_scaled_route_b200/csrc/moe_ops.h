@@ -28,6 +28,7 @@ struct GroupedParams {
   int32_t* status;
   int stream_w;             // weights are read about once: leave the L2 to the rows
   uint32_t idesc;
+  int split;                // CTAs that share a tile's contraction
 };
 
 struct WgradParams {
@@ -87,18 +88,46 @@ struct RowCombineBwdParams {
   float* dg;                // [T, k]
 };
 
-// How a call is tiled: rows of one tile (the rows side of the MMA), and CTAs
-// that work on a tile together.  tx has boxes of rows / ctas rows, txs of 32.
+// How a call is tiled: rows of one tile (the rows side of the MMA), CTAs of
+// one MMA, CTAs that share a tile's contraction, CTAs in all.  tx has boxes
+// of rows / ctas rows; txs, of 32, is used by pairs only.
 struct GroupedTile {
-  int rows, ctas;
+  int rows, ctas, split, grid;
 };
-GroupedTile grouped_tile(const GroupedParams& p);
+GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms);
 cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,
-                           const CUtensorMap& txs, const GroupedParams& p, int sms, cudaStream_t s);
+                           const CUtensorMap& txs, const GroupedParams& p, cudaStream_t s);
 cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const WgradParams& p, int sms, cudaStream_t s);
 cudaError_t launch_quant_int8(const QuantInt8Params& p, int dtype, cudaStream_t s);
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);
 cudaError_t launch_row_combine(const RowCombineParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_row_combine_bwd(const RowCombineBwdParams& p, int dtype, cudaStream_t s);
+
+// Launch as a programmatic dependent of the kernel before it in the stream
+// (the kernels wait, before they read anything, until that one is complete),
+// in clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                           cudaStream_t s, const Args&... args) {
+  if (smem > 48 * 1024) {  // the attribute belongs to the current device's context
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace moe

@@ -3,7 +3,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "moe_ops.h"
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -62,144 +65,341 @@ struct Vec {
   }
 };
 
+constexpr int kThreads = 256;
+constexpr int kFewSlots = 1184;  // 8 blocks on each of 148 SMs
+
 // ---- permute: y[p] = x[token(p)] ------------------------------------------------
-constexpr int kPermThreads = 256;
-__global__ void __launch_bounds__(kPermThreads) permute_kernel(const PermuteParams p) {
-  for (int pos = blockIdx.x; pos < p.rows; pos += gridDim.x) {
-    const long long t = slot_token(p.map, pos);
-    if (t < 0) continue;
-    const char* src = static_cast<const char*>(p.x) + t * p.ldx;
-    char* dst = static_cast<char*>(p.y) + (long long)pos * p.ldy;
-    const long long whole = p.row_bytes & ~15LL;
-    for (long long i = threadIdx.x * 16LL; i < whole; i += kPermThreads * 16LL)
-      *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
-    for (long long i = whole + threadIdx.x; i < p.row_bytes; i += kPermThreads) dst[i] = src[i];
+// W warps copy a row, each thread up to kCopies pieces of 16 bytes that are
+// all loaded before the first is stored.
+constexpr int kCopies = 4;
+template <int W>
+__global__ void __launch_bounds__(kThreads) permute_kernel(const PermuteParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int sub = threadIdx.x / (32 * W), i0 = threadIdx.x % (32 * W);
+  const long long pos = (long long)blockIdx.x * (kThreads / 32 / W) + sub;
+  if (pos >= p.rows) return;
+  const long long t = slot_token(p.map, (int)pos);
+  if (t < 0) return;
+  const char* src = static_cast<const char*>(p.x) + t * p.ldx;
+  char* dst = static_cast<char*>(p.y) + pos * p.ldy;
+  const long long whole = p.row_bytes & ~15LL;
+  for (long long base = (long long)blockIdx.y * (512 * W * kCopies); base < whole;
+       base += (long long)gridDim.y * (512 * W * kCopies)) {
+    uint4 v[kCopies];
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const long long at = base + (c * 32 * W + i0) * 16LL;
+      if (at < whole) v[c] = __ldg(reinterpret_cast<const uint4*>(src + at));
+    }
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const long long at = base + (c * 32 * W + i0) * 16LL;
+      if (at < whole) __stcs(reinterpret_cast<uint4*>(dst + at), v[c]);
+    }
   }
+  if (blockIdx.y == 0)
+    for (long long i = whole + i0; i < p.row_bytes; i += 32 * W) dst[i] = src[i];
 }
 
-// ---- combine: out[t] = sum_j g[t, j] y[inv[t, j]] (+ the shared expert's row) --
-constexpr int kCombThreads = 256;
+// 16 bytes of a row as loaded, to be unpacked later: several of them can be
+// in flight at a small cost in registers.
 template <typename T>
-__global__ void __launch_bounds__(kCombThreads) combine_kernel(const RowCombineParams p) {
-  __shared__ int pos[kMaxCombine];
-  __shared__ float wt[kMaxCombine];
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* row, int c, int n) {
+    if (c + Vec<T>::N <= n) {
+      u = __ldcs(reinterpret_cast<const uint4*>(row + c));
+    } else {
+      T e[Vec<T>::N];
+#pragma unroll
+      for (int i = 0; i < Vec<T>::N; ++i) e[i] = c + i < n ? row[c + i] : Elem<T>::put(0.0f);
+      u = *reinterpret_cast<const uint4*>(e);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const { return Elem<T>::get(reinterpret_cast<const T*>(&u)[i]); }
+};
+
+// ---- combine: out[t] = sum_j g[t, j] y[inv[t, j]] (+ the shared expert's row) --
+// One block per token and 256 pieces of 16 bytes of its columns; the rows of
+// kJoint slots are loaded together.
+constexpr int kJoint = 4;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int pos[kMaxCombine + kJoint];
+  __shared__ float wt[kMaxCombine + kJoint];
+  __shared__ int s_n;
   const int t = blockIdx.x;
-  const int n = p.k + p.n_shared;
-  if (threadIdx.x < n) {
+  if (threadIdx.x < 32) {
+    // the held slots in ascending order, closed up; lane 0 adds the shared expert's row
     const int j = threadIdx.x;
-    const bool routed = j < p.k;
-    pos[j] = p.inv[routed ? (size_t)t * p.k + j : (size_t)p.T * p.k + t];
-    wt[j] = routed && p.g ? p.g[(size_t)t * p.k + j] : 1.0f;
+    int at = j < p.k ? p.inv[(size_t)t * p.k + j] : -1;
+    const float g = j < p.k && p.g ? p.g[(size_t)t * p.k + j] : 1.0f;
+    if (at >= p.rows) at = -1;
+    const unsigned held = __ballot_sync(0xFFFFFFFFu, at >= 0);
+    if (at >= 0) {
+      const int i = __popc(held & ((1u << j) - 1u));
+      pos[i] = at;
+      wt[i] = g;
+    }
+    if (j == 0) {
+      int n = __popc(held);
+      if (p.n_shared) {
+        const int sh = p.inv[(size_t)p.T * p.k + t];
+        if (sh >= 0 && sh < p.rows) {
+          pos[n] = sh;
+          wt[n++] = 1.0f;
+        }
+      }
+      s_n = n;
+    }
   }
   __syncthreads();
+  const int n = s_n;
   T* out = static_cast<T*>(p.out) + t * p.ldo;
-  for (int c = threadIdx.x * Vec<T>::N; c < p.H; c += kCombThreads * Vec<T>::N) {
+  const T* y = static_cast<const T*>(p.y);
+  for (int c = (blockIdx.y * kThreads + threadIdx.x) * Vec<T>::N; c < p.H; c += gridDim.y * kThreads * Vec<T>::N) {
     Vec<T> acc;
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i) acc.v[i] = 0.0f;
-    for (int j = 0; j < n; ++j) {
-      if (pos[j] < 0 || pos[j] >= p.rows) continue;
-      Vec<T> y;
-      y.load(static_cast<const T*>(p.y) + pos[j] * p.ldy, c, p.H);
+    for (int j = 0; j < n; j += kJoint) {
+      Raw<T> r[kJoint];
 #pragma unroll
-      for (int i = 0; i < Vec<T>::N; ++i) acc.v[i] = fmaf(wt[j], y.v[i], acc.v[i]);
+      for (int q = 0; q < kJoint; ++q)
+        if (j + q < n) r[q].load(y + pos[j + q] * p.ldy, c, p.H);
+#pragma unroll
+      for (int q = 0; q < kJoint; ++q)
+        if (j + q < n) {
+          const float g = wt[j + q];
+#pragma unroll
+          for (int i = 0; i < Vec<T>::N; ++i) acc.v[i] = fmaf(g, r[q].get(i), acc.v[i]);
+        }
     }
     acc.store(out, c, p.H);
   }
 }
 
-// ---- its gradients: a warp per slot ----------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(kCombThreads) combine_bwd_kernel(const RowCombineBwdParams p) {
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = p.k + p.n_shared;
-  const T* dout = static_cast<const T*>(p.dout) + t * p.ldd;
-  for (int j = warp; j < n; j += kCombThreads / 32) {
-    const bool routed = j < p.k;
-    const size_t slot = routed ? (size_t)t * p.k + j : (size_t)p.T * p.k + t;
+// ---- its gradients: W warps per slot ----------------------------------------------
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const RowCombineBwdParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ float part[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long S = (long long)p.T * p.k, slots = S + (long long)p.n_shared * p.T;
+  const long long slot = (long long)blockIdx.x * (kThreads / 32 / W) + warp / W;
+  const bool routed = slot < S;
+  float dot = 0.0f;
+  if (slot < slots) {
     const int pos = p.inv[slot];
-    const bool held = pos >= 0 && pos < p.rows;
-    float dot = 0.0f;
-    if (held) {
+    if (pos >= 0 && pos < p.rows) {
+      const long long t = routed ? slot / p.k : slot - S;
+      const T* dout = static_cast<const T*>(p.dout) + t * p.ldd;
       const float g = routed ? p.g[slot] : 1.0f;
       const T* y = static_cast<const T*>(p.y) + pos * p.ldy;
       T* dy = static_cast<T*>(p.dy) + pos * p.lddy;
-      for (int c = lane * Vec<T>::N; c < p.H; c += 32 * Vec<T>::N) {
-        Vec<T> d, v;
-        d.load(dout, c, p.H);
-        if (routed) v.load(y, c, p.H);
+      constexpr int U = 4, N = Vec<T>::N, STEP = 32 * W * N;
+      for (int c0 = ((warp % W) * 32 + lane) * N; c0 < p.H; c0 += U * STEP) {
+        Raw<T> v[U];
+        Vec<T> d[U];
+        if (routed) {
 #pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) {
-          if (routed) dot = fmaf(d.v[i], v.v[i], dot);
-          d.v[i] *= g;
+          for (int u = 0; u < U; ++u)
+            if (c0 + u * STEP < p.H) v[u].load(y, c0 + u * STEP, p.H);
         }
-        d.store(dy, c, p.H);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * STEP < p.H) d[u].load(dout, c0 + u * STEP, p.H);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c0 + u * STEP >= p.H) continue;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (routed) dot = fmaf(d[u].v[i], v[u].get(i), dot);
+            d[u].v[i] *= g;
+          }
+          d[u].store(dy, c0 + u * STEP, p.H);
+        }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    if (routed && lane == 0) p.dg[slot] = dot;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  if (W > 1) {
+    if (lane == 0) part[warp] = dot;
+    __syncthreads();
+    dot = 0.0f;
+    for (int w = 0; w < W; ++w) dot += part[warp / W * W + w];
+  }
+  if (slot < slots && routed && lane == 0 && warp % W == 0) p.dg[slot] = dot;
 }
 
 // ---- row quantisation ---------------------------------------------------------------
-constexpr int kQ8Threads = 256;
-template <typename T>
-__global__ void __launch_bounds__(kQ8Threads) quant_int8_kernel(const QuantInt8Params p) {
-  __shared__ float red[kQ8Threads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int pos = blockIdx.x; pos < p.rows; pos += gridDim.x) {
-    const long long t = slot_token(p.map, pos);
-    if (t < 0) continue;
-    const T* x = static_cast<const T*>(p.x) + t * p.ldx;
-    int8_t* q = p.q + (long long)pos * p.ldq;
-    float amax = 0.0f;
-    for (int c = threadIdx.x; c < p.K; c += kQ8Threads) {
-      const float a = fabsf(Elem<T>::get(x[c]));
-      amax = a <= 3.402823466e38f ? fmaxf(amax, a) : __int_as_float(0x7F800000);  // NaN counts as infinite
-    }
+// 16 consecutive 16-bit values of a row, zeros past its end.
+struct Chunk {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const uint16_t* row, int c, int n) {
+    if (c + 16 <= n) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + c));
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(row + c) + 1);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (lane == 0) red[warp] = amax;
-    __syncthreads();
-    for (int w = 0; w < kQ8Threads / 32; ++w) amax = fmaxf(amax, red[w]);
-    __syncthreads();
-    const bool finite = amax <= 3.402823466e38f;
-    const float pre = amax > 1e30f ? 5.421010862e-20f : 1.0f;  // 2^-64: 127 times the largest bf16 overflows
-    for (int c = threadIdx.x; c < p.K; c += kQ8Threads) {
-      const float v = Elem<T>::get(x[c]);
-      q[c] = (finite && amax > 0.0f) ? (int8_t)__float2int_rn(__fdiv_rn(v * pre * 127.0f, amax * pre)) : (int8_t)0;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = c + 2 * i < n ? row[c + 2 * i] : 0, hi = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0;
+        w[i] = lo | hi << 16;
+      }
     }
-    if (threadIdx.x == 0)
-      p.s[pos] = !finite ? __int_as_float(0x7FC00000) : amax == 0.0f ? 1.0f : __fdiv_rn(amax, 127.0f);
   }
+};
+
+// The code of v * pre for a row maximum amax (both scaled by pre, a power of
+// two): rint(127 v / amax), ties to even.  fma(v, 127 / amax, 1.5 * 2^23)
+// leaves the rounded product in the low bits; the product is within 127 *
+// 1.5 * 2^-23 < 2.4e-5 of the quotient, so only a value that close to a tie
+// can be rounded to the wrong side, and those (1e-4 is tested) divide.  127 v
+// is exact for a 16-bit type, so the quotient's ties are seen as ties.
+__device__ __forceinline__ uint32_t code_int8(float v, float inv, float amax) {
+  const float magic = 12582912.0f;
+  float t = __fmaf_rn(v, inv, magic);
+  const float d = __fmaf_rn(v, inv, magic - t);
+  if (fabsf(d) > 0.4999f) t = rintf(__fdiv_rn(v * 127.0f, amax)) + magic;
+  return __float_as_uint(t) & 0xFFu;
+}
+
+// W warps per row; a thread keeps its first kKeep chunks between the two
+// passes and reads the others again.
+constexpr int kKeep = 2;
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) quant_int8_kernel(const QuantInt8Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ uint32_t red[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = threadIdx.x % (32 * W);
+  const long long pos = (long long)blockIdx.x * (kThreads / 32 / W) + warp / W;
+  const long long t = pos < p.rows ? slot_token(p.map, (int)pos) : -1;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + (t < 0 ? 0 : t) * p.ldx;
+  const int K = t < 0 ? 0 : p.K;
+  // magnitudes compare as their bits; an infinity or a NaN is above every finite value
+  Chunk keep[kKeep];
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if ((i0 + k * 32 * W) * 16 < K) keep[k].load(x, (i0 + k * 32 * W) * 16, K);
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if ((i0 + k * 32 * W) * 16 < K)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = __vmaxu2(top, keep[k].w[i] & 0x7FFF7FFFu);
+  for (int c = (i0 + kKeep * 32 * W) * 16; c < K; c += 32 * W * 16) {
+    Chunk v;
+    v.load(x, c, K);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v.w[i] & 0x7FFF7FFFu);
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (W > 1) {
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) top = max(top, red[warp / W * W + w]);
+  }
+  if (t < 0) return;
+  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+  const bool finite = top < (bf ? 0x7F80u : 0x7C00u);
+  const uint16_t top16 = (uint16_t)top;
+  const float amax = Elem<T>::get(*reinterpret_cast<const T*>(&top16));
+  // near the ends of bf16's range 127 v or 127 / amax leaves fp32's: move the row by 2^64
+  const float pre = !finite || amax == 0.0f ? 0.0f : amax > 1e30f ? 0x1p-64f : amax < 1e-30f ? 0x1p64f : 1.0f;
+  const float top_pre = amax * pre, inv = pre == 0.0f ? 0.0f : __fdiv_rn(127.0f, top_pre);
+  int8_t* q = p.q + pos * p.ldq;
+  auto put = [&](const Chunk& v, int c) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t b = 0;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint16_t raw = (uint16_t)(v.w[2 * i + h / 2] >> (16 * (h & 1)));
+        const float f = Elem<T>::get(*reinterpret_cast<const T*>(&raw));
+        b |= (pre == 0.0f ? 0u : code_int8(pre == 1.0f ? f : f * pre, inv, top_pre)) << (8 * h);
+      }
+      o[i] = b;
+    }
+    if (c + 16 <= K) {
+      *reinterpret_cast<uint4*>(q + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < K) q[c + i] = (int8_t)(o[i / 4] >> (8 * (i & 3)));
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if ((i0 + k * 32 * W) * 16 < K) put(keep[k], (i0 + k * 32 * W) * 16);
+  for (int c = (i0 + kKeep * 32 * W) * 16; c < K; c += 32 * W * 16) {
+    Chunk v;
+    v.load(x, c, K);
+    put(v, c);
+  }
+  if (i0 == 0) p.s[pos] = !finite ? __int_as_float(0x7FC00000) : amax == 0.0f ? 1.0f : __fdiv_rn(amax, 127.0f);
 }
 
 }  // namespace
 
+namespace {
+unsigned blocks(long long n, int per) { return (unsigned)((n + per - 1) / per); }
+
+template <typename T>
+cudaError_t quant_int8(const QuantInt8Params& p, cudaStream_t s) {
+  // the fewest warps that keep a row in registers
+  if (p.K <= 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 1>, blocks(p.rows, 8), kThreads, 0, 1, s, p);
+  else if (p.K <= 2 * 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 2>, blocks(p.rows, 4), kThreads, 0, 1, s, p);
+  else if (p.K <= 4 * 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 4>, blocks(p.rows, 2), kThreads, 0, 1, s, p);
+  else return launch_cluster(quant_int8_kernel<T, 8>, p.rows, kThreads, 0, 1, s, p);
+}
+
+template <typename T>
+cudaError_t row_combine(const RowCombineParams& p, cudaStream_t s) {
+  return launch_cluster(combine_kernel<T>, dim3(p.T, blocks(p.H, kThreads * Vec<T>::N)), kThreads, 0, 1, s, p);
+}
+
+template <typename T>
+cudaError_t row_combine_bwd(const RowCombineBwdParams& p, cudaStream_t s) {
+  const long long slots = (long long)p.T * (p.k + p.n_shared);
+  // few slots: a block each, so that a row's columns are read side by side
+  if (slots <= kFewSlots) return launch_cluster(combine_bwd_kernel<T, 8>, blocks(slots, 1), kThreads, 0, 1, s, p);
+  else return launch_cluster(combine_bwd_kernel<T, 1>, blocks(slots, 8), kThreads, 0, 1, s, p);
+}
+}  // namespace
+
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s) {
-  permute_kernel<<<p.rows, kPermThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.row_bytes <= 512 * kCopies) {
+    return launch_cluster(permute_kernel<1>, blocks(p.rows, 8), kThreads, 0, 1, s, p);
+  } else {
+    const unsigned chunks = blocks(p.row_bytes, 512 * 8 * kCopies);
+    return launch_cluster(permute_kernel<8>, dim3(p.rows, chunks < 64 ? chunks : 64), kThreads, 0, 1, s, p);
+  }
 }
 
 cudaError_t launch_row_combine(const RowCombineParams& p, int dtype, cudaStream_t s) {
-  if (dtype == MOE_DT_BF16) combine_kernel<__nv_bfloat16><<<p.T, kCombThreads, 0, s>>>(p);
-  else if (dtype == MOE_DT_FP16) combine_kernel<__half><<<p.T, kCombThreads, 0, s>>>(p);
-  else combine_kernel<float><<<p.T, kCombThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (dtype == MOE_DT_BF16) return row_combine<__nv_bfloat16>(p, s);
+  if (dtype == MOE_DT_FP16) return row_combine<__half>(p, s);
+  return row_combine<float>(p, s);
 }
 
 cudaError_t launch_row_combine_bwd(const RowCombineBwdParams& p, int dtype, cudaStream_t s) {
-  if (dtype == MOE_DT_BF16) combine_bwd_kernel<__nv_bfloat16><<<p.T, kCombThreads, 0, s>>>(p);
-  else if (dtype == MOE_DT_FP16) combine_bwd_kernel<__half><<<p.T, kCombThreads, 0, s>>>(p);
-  else combine_bwd_kernel<float><<<p.T, kCombThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (dtype == MOE_DT_BF16) return row_combine_bwd<__nv_bfloat16>(p, s);
+  if (dtype == MOE_DT_FP16) return row_combine_bwd<__half>(p, s);
+  return row_combine_bwd<float>(p, s);
 }
 
 cudaError_t launch_quant_int8(const QuantInt8Params& p, int dtype, cudaStream_t s) {
-  if (dtype == MOE_DT_BF16) quant_int8_kernel<__nv_bfloat16><<<p.rows, kQ8Threads, 0, s>>>(p);
-  else quant_int8_kernel<__half><<<p.rows, kQ8Threads, 0, s>>>(p);
-  return cudaGetLastError();
+  return dtype == MOE_DT_BF16 ? quant_int8<__nv_bfloat16>(p, s) : quant_int8<__half>(p, s);
 }
 
 }  // namespace moe

@@ -56,6 +56,9 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
   }
+  // everything above ran while the kernel before this one could still be
+  // running; nothing of its results is read before this point
+  griddep_wait();
   // unusable offsets (negative, falling, past P): nothing is computed
   int bad = 0;
   for (int e = threadIdx.x; e < p.E; e += C::THREADS) {
@@ -65,6 +68,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
   tc_fence_before();
   bad = __syncthreads_or(bad);
   tc_fence_after();
+  griddep_launch_dependents();  // (tensor memory is held: no later kernel can take it first)
   const uint32_t tmem = *tmem_holder;
   const int TN = (p.N + 127) / 128, TK = (p.K + C::BN - 1) / C::BN;
   const long long total = bad ? 0 : (long long)p.E * TN * TK;
@@ -220,10 +224,7 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const Wgr
                          cudaStream_t s) {
   WgradParams p = p0;
   p.idesc = idesc_f16(128, WCfg::BN, p.fmt, 1, 1);
-  const cudaError_t e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg::SMEM);
-  if (e != cudaSuccess) return e;
-  wgrad_kernel<<<sms, WCfg::THREADS, WCfg::SMEM, s>>>(ty, tx, p);
-  return cudaGetLastError();
+  return launch_cluster(wgrad_kernel, sms, WCfg::THREADS, WCfg::SMEM, 1, s, ty, tx, p);
 }
 
 }  // namespace moe

@@ -10,7 +10,6 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -402,14 +401,15 @@ class MoeLayer:
         if topk_ids.shape != (T, self.k):
             raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, {self.k}]")
         NG, P = self.E + self.n_shared, T * (self.k + self.n_shared)
-        with _launch("route", stream, topk_ids=(topk_ids, torch.int32)) as s:
-            if not topk_ids.is_contiguous():
-                raise ValueError("route: topk_ids is not contiguous")
-            counts, offsets, perm, inv = (torch.empty(n, dtype=torch.int32, device=topk_ids.device)
-                                          for n in (NG, NG + 1, P, P))
+        _vector(topk_ids, P - T * self.n_shared, "route: topk_ids")
+        dev = _device("route", ("topk_ids", topk_ids, torch.int32))
+
+        def body(s):
+            counts, offsets, perm, inv = (torch.empty(n, dtype=torch.int32, device=dev) for n in (NG, NG + 1, P, P))
             _check(moe_route(self.ctx, T, _ptr(topk_ids), _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv), s),
                    "moe_route")
-        return counts, offsets, perm, inv
+            return counts, offsets, perm, inv
+        return _call("route", dev, stream, body)
 
     def set_green_ctx(self, dispatch_sms):
         """Green-Context partition: dispatch kernels on >= dispatch_sms SMs, GEMMs on the rest (0 = off)."""
@@ -452,56 +452,68 @@ def finalize_bf16(acc, out=None, stream=None):
 
 
 # ---- expert operators on torch tensors (marshalling only) -----------------
-@contextlib.contextmanager
-def _launch(what, stream=None, **tensors):
-    """Checks tensors (name -> tensor, or (tensor, required dtype); None is skipped), makes their device current and
-    `stream` (default: that device's current stream) the one results are allocated on; yields the stream handle."""
-    import torch
+def _device(what, *tensors):
+    """The one CUDA device of `tensors`, each (name, tensor or None, required dtype or None)."""
     dev = None
-    for name, t in tensors.items():
-        t, dtype = t if isinstance(t, tuple) else (t, None)
+    for name, t, dtype in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{what}: {name} is not a CUDA tensor")
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{what}: {name} is on {t.device}, not on {dev}")
-        dev = t.device
+        d = t.device
+        if d != dev:
+            if d.type != "cuda":
+                raise ValueError(f"{what}: {name} is not a CUDA tensor")
+            if dev is not None:
+                raise ValueError(f"{what}: {name} is on {d}, not on {dev}")
+            dev = d
+    return dev
+
+
+def _call(what, dev, stream, body):
+    """body(stream handle) with `dev` current and `stream` (default: that device's current one) the stream that results
+    are allocated on."""
+    import torch
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return body(torch.cuda.current_stream(dev).cuda_stream)
     if stream is not None and stream.device != dev:
         raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {dev}")
-    with torch.cuda.device(dev), contextlib.ExitStack() as stack:
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream().cuda_stream
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return body(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _dtype_code(dtype, what):
     import torch
-    codes = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_FP16, torch.float32: MOE_DT_FP32}
-    if dtype not in codes:
-        raise ValueError(f"{what}: type {dtype} is not supported")
-    return codes[dtype]
+    if dtype == torch.bfloat16:
+        return MOE_DT_BF16
+    if dtype == torch.float16:
+        return MOE_DT_FP16
+    if dtype == torch.float32:
+        return MOE_DT_FP32
+    raise ValueError(f"{what}: type {dtype} is not supported")
 
 
 def _new_rows(rows, n, dtype, device):
     """An unset [rows, n] matrix whose row stride is a multiple of 16 bytes (contiguous where n allows it)."""
     import torch
     step = 16 // dtype.itemsize
+    if n % step == 0:
+        return torch.empty((rows, n), dtype=dtype, device=device)
     return torch.empty((rows, -(-n // step) * step), dtype=dtype, device=device)[:, :n]
 
 
 def _matrix(t, shape, what):
     """Row stride in elements of a matrix with contiguous rows; `shape` may hold None for any size."""
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple('any' if n is None else n for n in shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    got = t.shape
+    if len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got)):
+        raise ValueError(f"{what} has shape {tuple(got)}, not {tuple('any' if n is None else n for n in shape)}")
+    st = t.stride()
+    if st[-1] != 1 and got[-1] > 1:
         raise ValueError(f"{what}: rows are not contiguous")
-    if t.shape[-2] > 1:
-        return t.stride(-2)
+    if got[-2] > 1:
+        return st[-2]
     step = 16 // t.element_size()      # a single row: its stride is never used
-    return -(-t.shape[-1] // step) * step
+    return -(-got[-1] // step) * step
 
 
 def _vector(t, n, what):
@@ -509,34 +521,34 @@ def _vector(t, n, what):
         raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
 
 
-def _groups(offsets, E, what):
-    if offsets.dim() != 1 or offsets.shape[0] != E + 1 or not offsets.is_contiguous():
-        raise ValueError(f"{what}: offsets has shape {tuple(offsets.shape)}, not [{E + 1}]")
-
-
-def _weights(w, N, K, what):
-    """(row stride, expert stride) of [E, N, K] weights."""
-    ld = _matrix(w, (None, N, K), what)
-    return ld, (w.stride(0) if w.shape[0] > 1 else 0)
-
-
-def _grouped(entry, what, rows, name, w, offsets, R, M, out, out_dtype, status, stream):
-    import torch
-    P = rows.shape[0]
+def _weights(w, offsets, what):
+    """(E, N, K, row stride, expert stride) of the weights; offsets [E + 1] fit them."""
+    if w.dim() != 3:
+        raise ValueError(f"{what}: w has shape {tuple(w.shape)}, not [E, N, K]")
     E, N, K = w.shape
-    ld = _matrix(rows, (None, R), f"{what}: {name}")
-    ldw, sw = _weights(w, None, None, f"{what}: w")
-    _groups(offsets, E, what)
-    out_dtype = out.dtype if out is not None else (out_dtype or rows.dtype)
-    dt, odt = _dtype_code(rows.dtype, what), _dtype_code(out_dtype, what)
-    with _launch(what, stream, **{name: rows}, w=(w, rows.dtype), offsets=(offsets, torch.int32), out=out,
-                 status=(status, torch.int32)) as s:
-        if out is None:
-            out = _new_rows(P, M, out_dtype, rows.device)
-        ldo = _matrix(out, (P, M), f"{what}: out")
-        _check(entry(dt, odt, E, P, N, K, _ptr(offsets), _ptr(rows), ld, _ptr(w), ldw, sw, _ptr(out), ldo,
-                     _ptr(status), s), entry.__name__)
-    return out
+    if offsets is not None and (offsets.shape != (E + 1,) or not offsets.is_contiguous()):
+        raise ValueError(f"{what}: offsets has shape {tuple(offsets.shape)}, not [{E + 1}]")
+    return E, N, K, _matrix(w, (E, N, K), f"{what}: w"), (w.stride(0) if E > 1 else 0)
+
+
+def _grouped(entry, what, name, rows, contract, w, offsets, out, out_dtype, status, stream):
+    import torch
+    E, N, K, ldw, sw = _weights(w, offsets, what)
+    R, M = (K, N) if contract == "k" else (N, K)
+    P = rows.shape[0]
+    ld = _matrix(rows, (P, R), f"{what}: {name}")
+    dtype = rows.dtype
+    out_dtype = out.dtype if out is not None else (out_dtype or dtype)
+    dt, odt = _dtype_code(dtype, what), _dtype_code(out_dtype, what)
+    dev = _device(what, (name, rows, None), ("w", w, dtype), ("offsets", offsets, torch.int32), ("out", out, None),
+                  ("status", status, torch.int32))
+
+    def body(s):
+        y = _new_rows(P, M, out_dtype, dev) if out is None else out
+        _check(entry(dt, odt, E, P, N, K, _ptr(offsets), _ptr(rows), ld, _ptr(w), ldw, sw, _ptr(y),
+                     _matrix(y, (P, M), f"{what}: out"), _ptr(status), s), entry.__name__)
+        return y
+    return _call(what, dev, stream, body)
 
 
 def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=None):
@@ -545,18 +557,13 @@ def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=No
     x [P, K] and w [E, N, K] bf16 or fp16 with contiguous rows (any row and expert strides that are multiples of 16
     bytes), offsets device int32 [E+1]; out [P, N] in the same type or fp32.  Rows outside every group are left as
     they were (unspecified in an `out` made here).  status: optional device int32, see moe.h."""
-    if w.dim() != 3:
-        raise ValueError(f"grouped_gemm: w has shape {tuple(w.shape)}, not [E, N, K]")
-    return _grouped(moe_grouped_gemm, "grouped_gemm", x, "x", w, offsets, w.shape[2], w.shape[1], out, out_dtype,
-                    status, stream)
+    return _grouped(moe_grouped_gemm, "grouped_gemm", "x", x, "k", w, offsets, out, out_dtype, status, stream)
 
 
 def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, status=None, stream=None):
     """dx[p] = dy[p] w[e], the gradient of grouped_gemm for x (moe_grouped_gemm_dgrad): dy [P, N] -> [P, K]."""
-    if w.dim() != 3:
-        raise ValueError(f"grouped_gemm_dgrad: w has shape {tuple(w.shape)}, not [E, N, K]")
-    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", dy, "dy", w, offsets, w.shape[1], w.shape[2], out,
-                    out_dtype, status, stream)
+    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", "dy", dy, "n", w, offsets, out, out_dtype, status,
+                    stream)
 
 
 def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, stream=None):
@@ -566,19 +573,22 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
     what = "grouped_gemm_wgrad"
     lddy = _matrix(dy, (None, None), f"{what}: dy")
     ldx = _matrix(x, (dy.shape[0], None), f"{what}: x")
-    P, N, K, E = dy.shape[0], dy.shape[1], x.shape[1], offsets.shape[0] - 1
-    _groups(offsets, E, what)
-    out_dtype = out.dtype if out is not None else (out_dtype or dy.dtype)
-    dt, odt = _dtype_code(dy.dtype, what), _dtype_code(out_dtype, what)
-    with _launch(what, stream, dy=dy, x=(x, dy.dtype), offsets=(offsets, torch.int32), out=out,
-                 status=(status, torch.int32)) as s:
-        if out is None:
-            out = torch.empty((E, N, K), dtype=out_dtype, device=dy.device)
-        if out.shape != (E, N, K) or not out.is_contiguous():
-            raise ValueError(f"{what}: out is not contiguous [{E}, {N}, {K}]")
-        _check(moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, _ptr(offsets), _ptr(dy), lddy, _ptr(x), ldx, _ptr(out),
+    (P, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
+    _vector(offsets, E + 1, f"{what}: offsets")
+    dtype = dy.dtype
+    out_dtype = out.dtype if out is not None else (out_dtype or dtype)
+    dt, odt = _dtype_code(dtype, what), _dtype_code(out_dtype, what)
+    dev = _device(what, ("dy", dy, None), ("x", x, dtype), ("offsets", offsets, torch.int32), ("out", out, None),
+                  ("status", status, torch.int32))
+    if out is not None and (out.shape != (E, N, K) or not out.is_contiguous()):
+        raise ValueError(f"{what}: out is not contiguous [{E}, {N}, {K}]")
+
+    def body(s):
+        dw = torch.empty((E, N, K), dtype=out_dtype, device=dev) if out is None else out
+        _check(moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, _ptr(offsets), _ptr(dy), lddy, _ptr(x), ldx, _ptr(dw),
                                       _ptr(status), s), "moe_grouped_gemm_wgrad")
-    return out
+        return dw
+    return _call(what, dev, stream, body)
 
 
 def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
@@ -590,19 +600,19 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
     T, K = x.shape
     rows = T if perm is None else perm.shape[0]
     dt = _dtype_code(x.dtype, what)
-    with _launch(what, stream, x=x, perm=(perm, torch.int32), out=(out, torch.int8),
-                 scale=(scale, torch.float32)) as s:
-        if perm is not None:
-            _vector(perm, rows, f"{what}: perm")
-        if out is None:
-            out = _new_rows(rows, K, torch.int8, x.device)
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        ldq = _matrix(out, (rows, K), f"{what}: out")
-        _vector(scale, rows, f"{what}: scale")
-        _check(moe_quant_int8(dt, rows, K, T, k, _ptr(x), ldx, _ptr(perm), _ptr(out), ldq, _ptr(scale), s),
-               "moe_quant_int8")
-    return out, scale
+    dev = _device(what, ("x", x, None), ("perm", perm, torch.int32), ("out", out, torch.int8),
+                  ("scale", scale, torch.float32))
+    if perm is not None:
+        _vector(perm, rows, f"{what}: perm")
+
+    def body(s):
+        q = _new_rows(rows, K, torch.int8, dev) if out is None else out
+        sc = torch.empty(rows, dtype=torch.float32, device=dev) if scale is None else scale
+        _vector(sc, rows, f"{what}: scale")
+        _check(moe_quant_int8(dt, rows, K, T, k, _ptr(x), ldx, _ptr(perm), _ptr(q),
+                              _matrix(q, (rows, K), f"{what}: out"), _ptr(sc), s), "moe_quant_int8")
+        return q, sc
+    return _call(what, dev, stream, body)
 
 
 def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, status=None, stream=None):
@@ -612,29 +622,29 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
     dense product), offsets device int32 [E+1].  out [P, N] bf16 (default), fp16 or fp32."""
     import torch
     what = "int8_gemm"
-    if offsets is None and w.dim() == 2:
-        w = w[None]
-    if w.dim() != 3 or (offsets is None and w.shape[0] != 1):
-        raise ValueError(f"{what}: w has shape {tuple(w.shape)}; one matrix without offsets, [E, N, K] with them")
-    E, N, K = w.shape
-    ldq = _matrix(q, (None, K), f"{what}: q")
+    if offsets is None:
+        if w.dim() == 2:
+            w = w[None]
+        if w.dim() != 3 or w.shape[0] != 1:
+            raise ValueError(f"{what}: w has shape {tuple(w.shape)}; one matrix without offsets, [E, N, K] with them")
+    E, N, K, ldw, sw = _weights(w, offsets, what)
     P = q.shape[0]
-    ldw, sw = _weights(w, None, None, f"{what}: w")
-    if offsets is not None:
-        _groups(offsets, E, what)
+    ldq = _matrix(q, (P, K), f"{what}: q")
     _vector(q_scale, P, f"{what}: q_scale")
     _vector(w_scale, E * N, f"{what}: w_scale")
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     odt = _dtype_code(out_dtype, what)
-    with _launch(what, stream, q=(q, torch.int8), q_scale=(q_scale, torch.float32), w=(w, torch.int8),
-                 w_scale=(w_scale, torch.float32), offsets=(offsets, torch.int32), out=out,
-                 status=(status, torch.int32)) as s:
-        if out is None:
-            out = _new_rows(P, N, out_dtype, q.device)
-        ldo = _matrix(out, (P, N), f"{what}: out")
+    dev = _device(what, ("q", q, torch.int8), ("q_scale", q_scale, torch.float32), ("w", w, torch.int8),
+                  ("w_scale", w_scale, torch.float32), ("offsets", offsets, torch.int32), ("out", out, None),
+                  ("status", status, torch.int32))
+
+    def body(s):
+        y = _new_rows(P, N, out_dtype, dev) if out is None else out
         _check(moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), _ptr(q), ldq, _ptr(q_scale), _ptr(w), ldw, sw,
-                             _ptr(w_scale), _ptr(out), ldo, _ptr(status), s), "moe_int8_gemm")
-    return out
+                             _ptr(w_scale), _ptr(y), _matrix(y, (P, N), f"{what}: out"), _ptr(status), s),
+               "moe_int8_gemm")
+        return y
+    return _call(what, dev, stream, body)
 
 
 def permute(x, perm, k, out=None, stream=None):
@@ -645,14 +655,16 @@ def permute(x, perm, k, out=None, stream=None):
     ldx = _matrix(x, (None, None), f"{what}: x")
     T, H = x.shape
     rows = perm.shape[0]
+    _vector(perm, rows, f"{what}: perm")
     dt = _dtype_code(x.dtype, what)
-    with _launch(what, stream, x=x, perm=(perm, torch.int32), out=(out, x.dtype)) as s:
-        _vector(perm, rows, f"{what}: perm")
-        if out is None:
-            out = _new_rows(rows, H, x.dtype, x.device)
-        ldy = _matrix(out, (rows, H), f"{what}: out")
-        _check(moe_permute(dt, rows, H, T, k, _ptr(x), ldx, _ptr(perm), _ptr(out), ldy, s), "moe_permute")
-    return out
+    dev = _device(what, ("x", x, None), ("perm", perm, torch.int32), ("out", out, x.dtype))
+
+    def body(s):
+        y = _new_rows(rows, H, x.dtype, dev) if out is None else out
+        _check(moe_permute(dt, rows, H, T, k, _ptr(x), ldx, _ptr(perm), _ptr(y),
+                           _matrix(y, (rows, H), f"{what}: out"), s), "moe_permute")
+        return y
+    return _call(what, dev, stream, body)
 
 
 def _combine_sizes(inv, topk_w, k, n_shared, what):
@@ -679,13 +691,15 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
     rows, H = y.shape
     T, k = _combine_sizes(inv, topk_w, k, n_shared, what)
     dt = _dtype_code(y.dtype, what)
-    with _launch(what, stream, y=y, inv=(inv, torch.int32), topk_w=(topk_w, torch.float32), out=(out, y.dtype)) as s:
-        if out is None:
-            out = _new_rows(T, H, y.dtype, y.device)
-        ldo = _matrix(out, (T, H), f"{what}: out")
-        _check(moe_combine(dt, rows, H, T, k, n_shared, _ptr(y), ldy, _ptr(inv), _ptr(topk_w), _ptr(out), ldo, s),
-               "moe_combine")
-    return out
+    dev = _device(what, ("y", y, None), ("inv", inv, torch.int32), ("topk_w", topk_w, torch.float32),
+                  ("out", out, y.dtype))
+
+    def body(s):
+        o = _new_rows(T, H, y.dtype, dev) if out is None else out
+        _check(moe_combine(dt, rows, H, T, k, n_shared, _ptr(y), ldy, _ptr(inv), _ptr(topk_w), _ptr(o),
+                           _matrix(o, (T, H), f"{what}: out"), s), "moe_combine")
+        return o
+    return _call(what, dev, stream, body)
 
 
 def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, stream=None):
@@ -698,14 +712,15 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     rows, H = y.shape
     ldd = _matrix(dout, (T, H), f"{what}: dout")
     dt = _dtype_code(y.dtype, what)
-    with _launch(what, stream, y=y, dout=(dout, y.dtype), inv=(inv, torch.int32), topk_w=(topk_w, torch.float32),
-                 dy=(dy, y.dtype), dtopk_w=(dtopk_w, torch.float32)) as s:
-        if dy is None:
-            dy = _new_rows(rows, H, y.dtype, y.device)
-        if dtopk_w is None:
-            dtopk_w = torch.empty((T, k), dtype=torch.float32, device=y.device)
-        lddy = _matrix(dy, (rows, H), f"{what}: dy")
-        _vector(dtopk_w, T * k, f"{what}: dtopk_w")
+    dev = _device(what, ("y", y, None), ("dout", dout, y.dtype), ("inv", inv, torch.int32),
+                  ("topk_w", topk_w, torch.float32), ("dy", dy, y.dtype), ("dtopk_w", dtopk_w, torch.float32))
+
+    def body(s):
+        gy = _new_rows(rows, H, y.dtype, dev) if dy is None else dy
+        gw = torch.empty((T, k), dtype=torch.float32, device=dev) if dtopk_w is None else dtopk_w
+        _vector(gw, T * k, f"{what}: dtopk_w")
         _check(moe_combine_backward(dt, rows, H, T, k, n_shared, _ptr(dout), ldd, _ptr(y), ldy, _ptr(inv),
-                                    _ptr(topk_w), _ptr(dy), lddy, _ptr(dtopk_w), s), "moe_combine_backward")
-    return dy, dtopk_w
+                                    _ptr(topk_w), _ptr(gy), _matrix(gy, (rows, H), f"{what}: dy"), _ptr(gw), s),
+               "moe_combine_backward")
+        return gy, gw
+    return _call(what, dev, stream, body)
