@@ -164,36 +164,30 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   const int kb1 = SPLIT ? (int)((long long)chunks * (rank + 1) / split) : chunks;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = p.stream_w ? policy_evict_first() : policy_evict_normal();
-      const uint64_t pol_x = policy_evict_normal();
-      const uint32_t full0 = CG == 2 ? mapa_rank(full, 0) : smem_u32(full);
-      uint32_t armed = 0, parity = 0;
-      bool ok = true;
-      int it = 0, e = 0;
-      for (int u = team; u < work.total && ok; u += teams) {
-        const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
-        if (t.rows <= 0) continue;
-        // the MMA covers the tile's rows rounded up; each CTA of a pair
-        // holds half of them, in small boxes unless the tile is full
-        const int n = CG == 2 ? (t.rows + 31) & ~31 : BN;
-        const int boxes = CG == 1 || n == BN ? 0 : (n / 2 + C::BOX - 1) / C::BOX;
-        const uint32_t bytes = CG == 1 || n == BN ? CG * C::STAGE : 2 * (C::A_BYTES + boxes * C::BOX * 128);
-        const int half = CG == 2 ? (int)rank : 0;
-        const int m0 = t.m0 + half * 128, p0 = t.p0 + half * (n / CG);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % STAGES;
-          const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol_w = p.stream_w ? policy_evict_first() : policy_evict_normal();
+    const uint64_t pol_x = policy_evict_normal();
+    const uint32_t full0 = CG == 2 ? mapa_rank(full, 0) : smem_u32(full);
+    uint32_t armed = 0, st = 0, ph = 0;
+    bool ok = true;
+    int e = 0;
+    for (int u = team; u < work.total && ok; u += teams) {
+      const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+      if (t.rows <= 0) continue;
+      // the MMA covers the tile's rows rounded up; each CTA of a pair
+      // holds half of them, in small boxes unless the tile is full
+      const int n = CG == 2 ? (t.rows + 31) & ~31 : BN;
+      const int boxes = CG == 1 || n == BN ? 0 : (n / 2 + C::BOX - 1) / C::BOX;
+      const uint32_t bytes = CG == 1 || n == BN ? CG * C::STAGE : 2 * (C::A_BYTES + boxes * C::BOX * 128);
+      const int half = CG == 2 ? (int)rank : 0;
+      const int m0 = t.m0 + half * 128, p0 = t.p0 + half * (n / CG);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = mbar_wait_warp(&empty[st], ph ^ 1u, abort);
+        if (!ok) break;
+        uint8_t* a = smem + st * C::STAGE;
+        const int r0 = kb * C::CH;
+        if (elect_one()) {
           // the even CTA posts the bytes of both
           if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
-          armed |= 1u << st;
-          parity = (parity & ~(1u << st)) | (ph << st);
-          uint8_t* a = smem + st * C::STAGE;
-          const int r0 = kb * C::CH;
           if constexpr (CG == 1) {
             if (KIND == GG_DGRAD) {
               tma_load_3d(&tmW, &full[st], a, m0, r0, t.e, pol_w);
@@ -215,57 +209,63 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
               tma_load_2d_pair(&tmXs, bar, a + C::A_BYTES + b * C::BOX * 128, r0, p0 + b * C::BOX, pol_x);
           }
         }
+        armed |= 1u << st;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
-      // after an abort: the copies in flight land before the CTAs leave (the
-      // even CTA's barriers count both CTAs' bytes)
-      if (*abort && (CG == 1 || rank == 0))
-        for (int s = 0; s < STAGES; ++s)
-          if (armed & (1u << s)) mbar_drain(&full[s], (parity >> s) & 1u);
     }
+    // after an abort: the copies in flight land before the CTAs leave (the
+    // even CTA's barriers count both CTAs' bytes).  Stages below st were last
+    // armed with parity ph, the others with the parity before.
+    if (*abort && (CG == 1 || rank == 0))
+      for (uint32_t s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) mbar_drain(&full[s], s < st ? ph : ph ^ 1u);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && (CG == 1 || rank == 0)) {
-      const uint32_t empty1 = CG == 2 ? mapa_rank(empty, 1) : 0, tfull1 = CG == 2 ? mapa_rank(tfull, 1) : 0;
+    if (CG == 1 || rank == 0) {
+      const uint32_t empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), a0 = smem_u32(smem);
+      const uint64_t ad0 = KIND == GG_DGRAD ? sdesc_mn_sw128(a0, C::A_BYTES / 2) : sdesc_k_sw128(a0);
+      const uint64_t bd0 = sdesc_k_sw128(a0 + C::A_BYTES);
+      // an instruction takes 32 bytes of the contraction, or 16 rows of 128 bytes
+      constexpr uint64_t step_a = KIND == GG_DGRAD ? 128 : 2, step_b = 2;
       bool ok = true;
-      int it = 0, j = 0, e = 0;
-      for (int u = team; u < work.total && ok; u += teams) {
-        const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
-        if (t.rows <= 0) continue;
+      uint32_t st = 0, ph = 0;
+      int j = 0, e = 0, u = team;
+      Tile next = {};
+      if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+      while (u < work.total && ok) {
+        const Tile t = next;
+        u += teams;
+        if (t.rows <= 0) {
+          if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+          continue;
+        }
         const int n = (t.rows + 16 * CG - 1) & ~(16 * CG - 1);
         const uint32_t idesc = p.idesc | (uint32_t)(n >> 3) << 17;
         const int buf = j & 1;
-        ok = mbar_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
+        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
         if (!ok) break;
         tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % STAGES;
-          if (!mbar_wait(&full[st], (uint32_t)(it / STAGES) & 1u, abort)) {
-            ok = false;
-            break;
-          }
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait_warp(&full[st], ph, abort);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + st * C::STAGE);
-          const uint64_t ad = KIND == GG_DGRAD ? sdesc_mn_sw128(a, C::A_BYTES / 2) : sdesc_k_sw128(a);
-          const uint64_t bd = sdesc_k_sw128(a + C::A_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            // 32 bytes of the contraction per instruction, or 16 rows of 128 bytes
-            const uint64_t da = ad + (KIND == GG_DGRAD ? 128 * kk : 2 * kk);
-            if (KIND == GG_INT8)
-              mma_s8<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb != kb0) | (kk != 0));
-            else
-              mma_f16<CG>(tmem + buf * BN, da, bd + 2 * kk, idesc, (kb != kb0) | (kk != 0));
+          const uint64_t off = st * (C::STAGE >> 4);
+          mma_steps4<KIND == GG_INT8, CG>(tmem + buf * BN, ad0 + off, bd0 + off, step_a, step_b, idesc, kb != kb0);
+          mma_commit_all<CG>(empty0 + 8u * st);
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
           }
-          mma_commit_at<CG>(smem_u32(&empty[st]));
-          if (CG == 2) mma_commit_at<CG>(empty1 + 8u * st);
+          // the next tile is looked up while the tensor cores have work
+          if (kb == kb0 && u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
         }
-        if (ok) {
-          mma_commit_at<CG>(smem_u32(&tfull[buf]));
-          if (CG == 2) mma_commit_at<CG>(tfull1 + 8u * buf);
-        }
+        if (ok) mma_commit_all<CG>(tfull0 + 8u * buf);
         ++j;
       }
-      mma_commit_at<CG>(smem_u32(done));
+      mma_commit_all<CG>(smem_u32(done));
       mbar_drain(done, 0);
     }
     __syncwarp();

@@ -43,6 +43,27 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_
       : "memory");
 }
 
+// Store of a box from shared memory; what lies outside the tensor is dropped.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until at most N of this thread's stores still read shared memory / are
+// incomplete.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Order this thread's writes to its shared memory before the asynchronous
+// proxy's (TMA's, the tensor cores') accesses that follow.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ uint64_t policy_evict_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -79,41 +100,57 @@ __host__ __device__ constexpr uint32_t idesc_s8(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One MMA of a CTA (CG = 1) or of the pair (CG = 2: M / 2 rows of A and N / 2
-// rows of B in each CTA, M / 2 accumulator rows in each).
-template <int CG>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+// ---- issue ----------------------------------------------------------------------
+// The issuing warps run their loops with all 32 lanes (so that addresses and
+// descriptors stay in uniform registers) and let one elected lane issue:
+// with the loop inside `if (lane == 0)` a pipeline step of four MMAs took
+// 680 cycles of issue on B200 instead of about 400, more than the 512 that
+// the MMAs themselves need.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
-template <int CG>
-__device__ __forceinline__ void mma_s8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+
+// STEPS MMAs along the contraction, each `sa` / `sb` (descriptor units) after
+// the last; the first one overwrites the accumulator unless `accumulate`.  CG
+// = 1: of this CTA; CG = 2: of the pair (M / 2 rows of A and N / 2 rows of B
+// in each CTA, M / 2 accumulator rows in each).  Called by a whole warp.
+#define MOE_MMA_STEPS(GROUP, KIND)                                                                       \
+  asm volatile(                                                                                          \
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                                   \
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"                                                                  \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                        \
+      "add.u64 a1, %1, %3;\n\tadd.u64 a2, a1, %3;\n\tadd.u64 a3, a2, %3;\n\t"                            \
+      "add.u64 b1, %2, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"                            \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %5, p;\n\t"                      \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a1, b1, %5, 1;\n\t"                      \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a2, b2, %5, 1;\n\t"                      \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a3, b3, %5, 1;\n\t}\n" ::"r"(d),         \
+      "l"(a), "l"(b), "l"(sa), "l"(sb), "r"(idesc), "r"(accumulate)                                      \
+      : "memory")
+template <bool INT8, int CG>
+__device__ __forceinline__ void mma_steps4(uint32_t d, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb,
+                                           uint32_t idesc, uint32_t accumulate) {
+  if constexpr (INT8 && CG == 1) MOE_MMA_STEPS("1", "i8");
+  if constexpr (INT8 && CG == 2) MOE_MMA_STEPS("2", "i8");
+  if constexpr (!INT8 && CG == 1) MOE_MMA_STEPS("1", "f16");
+  if constexpr (!INT8 && CG == 2) MOE_MMA_STEPS("2", "f16");
+}
+#undef MOE_MMA_STEPS
+// One MMA of the pair on 16-bit operands, by a whole warp.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // ---- CTA pairs ------------------------------------------------------------------
@@ -158,16 +195,24 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
-// Arrive on the barrier at a cluster address once the MMAs issued so far by
-// this thread completed.
+// Arrive on a barrier (in both CTAs of a pair, at the same place) once the
+// MMAs that this warp's elected lane issued so far completed.  Called by a
+// whole warp.  One commit for both CTAs: a commit each costs the issuing warp
+// another 60 cycles per step.
 template <int CG>
-__device__ __forceinline__ void mma_commit_at(uint32_t bar_cluster) {
+__device__ __forceinline__ void mma_commit_all(uint32_t bar) {
   if constexpr (CG == 1)
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar_cluster)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+        : "memory");
   else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar_cluster)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+            bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst, uint32_t ncols) {
@@ -188,6 +233,10 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) 
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// mbar_wait by a whole warp: false for every lane if it gave up for one.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
+}
 // Bounded wait used while draining: like mbar_wait, but blind to the abort word.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();

@@ -57,7 +57,9 @@ int elem_size(int dtype) {
 bool is16(int dtype) { return dtype == MOE_DT_BF16 || dtype == MOE_DT_FP16; }
 
 CUtensorMapDataType map_type(int dtype) {
-  return dtype == MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return dtype == MOE_DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 }
 
 // A row stride in elements: at least the row, a multiple of 16 bytes, within TMA's limit.
@@ -163,17 +165,19 @@ moe_status moe_grouped_gemm_wgrad(int dtype, int out_dtype, int E, int P, int N,
   int sms = 0;
   const moe_status ds = device_sms(&sms);
   if (ds != MOE_OK) return ds;
+  if ((long long)E * ((N + 255) / 256) * ((K + 255) / 256) > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   moe::WgradParams p{};
   p.E = E; p.P = P; p.N = N; p.K = K;
   p.offsets = offsets;
   p.dw = dw; p.out_type = out_dtype;
   p.fmt = dtype == MOE_DT_BF16 ? 1 : 0;
   p.status = d_status;
-  CUtensorMap ty, tx;
+  CUtensorMap ty, tx, to;
   if (!make_map(&ty, map_type(dtype), 2, dy, N, P, lddy, 0, 0, 64) ||
-      !make_map(&tx, map_type(dtype), 2, x, K, P, ldx, 0, 0, 64))
+      !make_map(&tx, map_type(dtype), 2, x, K, P, ldx, 0, 0, 64) ||
+      !make_map(&to, map_type(out_dtype), oes, dw, K, N, K, E, (long long)N * K, 32))
     return MOE_ERR_CUDA;
-  return moe::launch_wgrad(ty, tx, p, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return moe::launch_wgrad(ty, tx, to, p, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_int8_gemm(int out_dtype, int E, int P, int N, int K, const int32_t* offsets, const int8_t* q,

@@ -5,57 +5,128 @@
 namespace moe {
 namespace {
 
-// The contraction runs over rows, so both operands have their output index
-// contiguous (MN-major).  A stage holds 64 rows of 128 dy columns (two boxes
-// of 64) and of BN x columns (BN / 64 boxes).
+// A pair of CTAs computes 256 output rows n by 256 columns k: each holds 128
+// of the rows (accumulators in its tensor memory, double-buffered) and loads
+// half of both operands.  The contraction runs over the group's rows, so both
+// operands have their output index contiguous (MN-major): a stage holds 64
+// rows of 128 dy columns and of 128 x columns, in boxes of 64 columns whose
+// rows are 128-byte lines.
+//
+// Warp 0 loads, warp 1 (of the even CTA) issues the MMAs, warps 4-11 read the
+// accumulators, round them and store them by TMA from shared memory.
 struct WCfg {
-  static constexpr int THREADS = 256;
-  static constexpr int BN = 256;
-  static constexpr int CH = 64;
-  static constexpr int BOX = 64 * 128;
-  static constexpr int NA = 2, NB = BN / 64;
-  static constexpr int STAGE = (NA + NB) * BOX;
-  static constexpr int STAGES = 4;
-  static constexpr int TMEM_COLS = 512;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int BM = 256, BN = 256;
+  static constexpr int CH = 64;        // rows per stage
+  static constexpr int BOX = CH * 128;
+  static constexpr int STAGE = 4 * BOX;  // dy: boxes 0, 1; x: boxes 2, 3
+  static constexpr int STAGES = 5;
+  static constexpr int OUT = 32 * 128;  // per epilogue warp: a box of 32 rows of 128 bytes
+  static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int BARS = 512;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + BARS;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * OUT + BARS;  // (+ the offsets)
+  static_assert((4 * STAGES + 5) * 8 + 8 <= BARS && SMEM + kMaxGroups * 4 <= 232448, "shared memory");
+};
+
+// Work of one pair: all features of an expert before the next column of
+// tiles, all tiles of an expert before the next expert.  The units of the
+// last, partial wave are halves of 128 columns when they still are one wave.
+struct WUnit {
+  int e, lo, hi;  // expert, its rows
+  int n0, k0, nb; // first row and column of the output, 128-column halves
+};
+struct WWalk {
+  const int* s_off;
+  int TN, per, K, whole, halves, total;
+  int u, r, e;  // next unit; its place within expert e
+  __device__ __forceinline__ WWalk(const int* off, int E, int N, int K_, int team, int teams) : s_off(off), K(K_) {
+    TN = (N + WCfg::BM - 1) / WCfg::BM;
+    per = TN * ((K + WCfg::BN - 1) / WCfg::BN);
+    total = E * per;
+    const int rem = total % teams;
+    whole = total - rem;
+    halves = rem * 2 <= teams;
+    if (halves) total = whole + 2 * rem;
+    u = team;
+    r = team;
+    e = 0;
+  }
+  __device__ __forceinline__ bool take(WUnit& t, int teams) {
+    if (u >= total) return false;
+    int at = r, half = 0;
+    if (halves && u >= whole) {
+      // (the walk passes `whole` once: r is u's place counted from expert e)
+      half = (u - whole) & 1;
+      at = r - (u - whole) + ((u - whole) >> 1);
+    }
+    int ee = e;
+    while (at >= per) {
+      at -= per;
+      ++ee;
+    }
+    t.e = ee;
+    t.lo = s_off[ee];
+    t.hi = s_off[ee + 1];
+    t.n0 = (at % TN) * WCfg::BM;
+    t.k0 = (at / TN) * WCfg::BN;
+    t.nb = K - t.k0 > 128 ? 2 : 1;
+    if (halves && u >= whole) {
+      t.nb = 1;
+      t.k0 += half * 128;  // (past K: nothing is loaded, computed or stored)
+    }
+    u += teams;
+    r += teams;
+    if (u < whole)
+      while (r >= per) {
+        r -= per;
+        ++e;
+      }
+    return true;
+  }
 };
 
 __global__ void __launch_bounds__(WCfg::THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
-                 const WgradParams p) {
+                 const __grid_constant__ CUtensorMap tmO, const WgradParams p) {
   using C = WCfg;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
+  uint8_t* out = smem + STAGES * C::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + C::EPI_WARPS * C::OUT);  // (even CTA) both CTAs' bytes
+  uint64_t* empty = full + STAGES;      // a commit to each CTA
+  uint64_t* part = empty + STAGES;      // this CTA's bytes of a stage whose tail has to be zeroed
+  uint64_t* zeroed = part + STAGES;     // (even CTA) both CTAs have zeroed the tail
+  uint64_t* tfull = zeroed + STAGES;    // a commit to each CTA
+  uint64_t* tempty = tfull + 2;         // (even CTA) the epilogue warps of both CTAs
   uint64_t* done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + C::BARS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int team = blockIdx.x / 2, teams = gridDim.x / 2;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&part[s], 1);
+      mbar_init(&zeroed[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], 2 * C::EPI_WARPS);
     }
     mbar_init(done, 1);
     *abort = 0;
     mbar_fence_init();
     tma_prefetch_map(&tmY);
     tma_prefetch_map(&tmX);
+    tma_prefetch_map(&tmO);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, C::TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_cg<2>(tmem_holder, C::TMEM_COLS);
   // everything above ran while the kernel before this one could still be
   // running; nothing of its results is read before this point
   griddep_wait();
@@ -64,154 +135,208 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
   for (int e = threadIdx.x; e < p.E; e += C::THREADS) {
     const int lo = p.offsets[e], hi = p.offsets[e + 1];
     bad |= (lo < 0) | (hi < lo) | (hi > p.P);
+    s_off[e] = lo;
+    if (e == p.E - 1) s_off[p.E] = hi;
   }
   tc_fence_before();
   bad = __syncthreads_or(bad);
+  cluster_sync_all();  // both CTAs' barriers exist before any signal crosses
   tc_fence_after();
   griddep_launch_dependents();  // (tensor memory is held: no later kernel can take it first)
   const uint32_t tmem = *tmem_holder;
-  const int TN = (p.N + 127) / 128, TK = (p.K + C::BN - 1) / C::BN;
-  const long long total = bad ? 0 : (long long)p.E * TN * TK;
+  // (a unit's place in the walk: the same for every role)
+  WWalk walk(s_off, bad ? 0 : p.E, p.N, p.K, team, teams);
+  // A stage's last rows are zeroed when they end inside a 16-row MMA step.
+  auto ragged = [](int held) { return held < C::CH && (held & 15); };
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_normal();
-      uint32_t armed = 0, parity = 0;
-      bool ok = true;
-      int it = 0;
-      for (long long u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const int e = (int)(u / (TN * TK)), r = (int)(u % (TN * TK));
-        const int n0 = (r % TN) * 128, k0 = (r / TN) * C::BN;
-        const int lo = p.offsets[e], hi = p.offsets[e + 1];
-        for (int row = lo; row < hi; row += C::CH, ++it) {
-          const int st = it % STAGES;
-          const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
-            ok = false;
-            break;
+    const uint64_t pol = policy_evict_normal();
+    const uint32_t full0 = mapa_rank(full, 0), part0 = mapa_rank(part, rank);
+    uint32_t armed = 0, armed_part = 0, uses = 0, st = 0, ph = 0;
+    bool ok = true;
+    WUnit t;
+    while (ok && walk.take(t, teams)) {
+      if (t.k0 >= p.K) continue;
+      const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 64 * t.nb, nb = t.nb;
+      const uint32_t bytes = (2 + nb) * C::BOX;
+      for (int row = t.lo; row < t.hi; row += C::CH) {
+        ok = mbar_wait_warp(&empty[st], ph ^ 1u, abort);
+        if (!ok) break;
+        const bool rag = ragged(t.hi - row);
+        const uint32_t bar = (rag ? part0 : full0) + 8u * st;
+        uint8_t* a = smem + st * C::STAGE;
+        if (elect_one()) {
+          if (rag) {
+            if (rank == 0) mbar_arrive(&full[st]);  // (no bytes: this phase only counts along)
+            mbar_arrive_expect_tx(&part[st], bytes);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&full[st], 2 * bytes);
           }
-          mbar_arrive_expect_tx(&full[st], C::STAGE);
-          armed |= 1u << st;
-          parity = (parity & ~(1u << st)) | (ph << st);
-          uint8_t* a = smem + st * C::STAGE;
-#pragma unroll
-          for (int b = 0; b < C::NA; ++b) tma_load_2d(&tmY, &full[st], a + b * C::BOX, n0 + 64 * b, row, pol);
-#pragma unroll
-          for (int b = 0; b < C::NB; ++b)
-            tma_load_2d(&tmX, &full[st], a + (C::NA + b) * C::BOX, k0 + 64 * b, row, pol);
+          tma_load_2d_pair(&tmY, bar, a, n0, row, pol);
+          tma_load_2d_pair(&tmY, bar, a + C::BOX, n0 + 64, row, pol);
+          tma_load_2d_pair(&tmX, bar, a + 2 * C::BOX, k0, row, pol);
+          if (nb == 2) tma_load_2d_pair(&tmX, bar, a + 3 * C::BOX, k0 + 64, row, pol);
+        }
+        armed |= 1u << st;
+        if (rag) {
+          armed_part |= 1u << st;
+          uses ^= 1u << st;
+        }
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
         }
       }
-      if (*abort)
-        for (int s = 0; s < STAGES; ++s)
-          if (armed & (1u << s)) mbar_drain(&full[s], (parity >> s) & 1u);
     }
+    // after an abort: the copies in flight land before the CTAs leave.
+    // Stages below st were last armed with parity ph, the others before.
+    if (*abort)
+      for (uint32_t s = 0; s < STAGES; ++s) {
+        if (rank == 0 && armed & (1u << s)) mbar_drain(&full[s], s < st ? ph : ph ^ 1u);
+        if (armed_part & (1u << s)) mbar_drain(&part[s], ((uses >> s) & 1u) ^ 1u);
+      }
     __syncwarp();
   } else if (warp == 1) {
+    const uint32_t empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), zeroed0 = mapa_rank(zeroed, 0);
+    const uint64_t ad0 = sdesc_mn_sw128(smem_u32(smem), C::BOX);
+    const uint64_t bd0 = sdesc_mn_sw128(smem_u32(smem) + 2 * C::BOX, C::BOX);
+    uint32_t uses = 0;  // parity of each stage's next use of part / zeroed
+    uint32_t st = 0, ph = 0;
     bool ok = true;
-    int it = 0, j = 0;
-    for (long long u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const int e = (int)(u / (TN * TK));
-      const int lo = p.offsets[e], hi = p.offsets[e + 1];
-      if (hi == lo) continue;
+    int j = 0;
+    WUnit next;
+    bool more = walk.take(next, teams);
+    while (more && ok) {
+      const WUnit t = next;
+      const int lo = t.lo, hi = t.hi, nb = t.nb;
+      if (hi == lo || t.k0 >= p.K) {
+        more = walk.take(next, teams);
+        continue;
+      }
+      const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
       const int buf = j & 1;
-      ok = mbar_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      for (int row = lo; row < hi; row += C::CH, ++it) {
-        const int st = it % STAGES;
-        ok = mbar_wait(&full[st], (uint32_t)(it / STAGES) & 1u, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+      if (rank == 0) {
+        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
         if (!ok) break;
-        uint8_t* a = smem + st * C::STAGE;
+        tc_fence_after();
+      }
+      for (int row = lo; row < hi; row += C::CH) {
         const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
-        if (held & 15) {
+        if (ragged(hi - row)) {
           // The last step's rows past the group's end belong to the next
           // group (or to no one) and may hold anything, NaN too: zeros in
           // both operands.  A row is one 128-byte line of each box, whatever
           // the swizzle does inside it.
-          const int lines = steps * 16 - held;
-          for (int i = lane; i < lines * 8 * (C::NA + C::NB); i += 32) {
-            const int b = i / (lines * 8), in = i % (lines * 8);
-            *reinterpret_cast<uint4*>(a + b * C::BOX + held * 128 + in * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          uint8_t* a = smem + st * C::STAGE;
+          const uint32_t use = (uses >> st) & 1u;
+          uses ^= 1u << st;
+          ok = mbar_wait_warp(&part[st], use, abort);
+          if (!ok) break;
+          const int pieces = (steps * 16 - held) * 8;
+          for (int i = lane; i < pieces * (2 + nb); i += 32)
+            *reinterpret_cast<uint4*>(a + (i / pieces) * C::BOX + held * 128 + (i % pieces) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
           __syncwarp();
+          if (lane == 0) mbar_arrive_at(zeroed0 + 8u * st);
+          if (rank == 0) {
+            ok = mbar_wait_cluster(&zeroed[st], use, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+          }
         }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t ad = sdesc_mn_sw128(smem_u32(a), C::BOX);
-          const uint64_t bd = sdesc_mn_sw128(smem_u32(a + C::NA * C::BOX), C::BOX);
-          for (int kk = 0; kk < steps; ++kk)
-            mma_f16<1>(tmem + buf * C::BN, ad + 128 * kk, bd + 128 * kk, p.idesc, (row != lo) | (kk != 0));
-          mma_commit(&empty[st]);
+        if (rank == 0) {
+          ok = mbar_wait_warp(&full[st], ph, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t off = st * (C::STAGE >> 4);
+          const uint32_t d = tmem + buf * C::BN;
+          if (steps == 4) {
+            mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, row != lo);
+          } else {
+            for (int kk = 0; kk < steps; ++kk)
+              mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != lo) | (kk != 0));
+          }
+          mma_commit_all<2>(empty0 + 8u * st);
         }
-        __syncwarp();
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+        // the next unit is looked up while the tensor cores have work
+        if (row == lo) more = walk.take(next, teams);
       }
-      if (ok && lane == 0) mma_commit(&tfull[buf]);
-      __syncwarp();
+      if (ok && rank == 0) mma_commit_all<2>(tfull0 + 8u * buf);
       ++j;
     }
-    if (lane == 0) mma_commit(done);
+    if (rank == 0) {
+      mma_commit_all<2>(smem_u32(done));
+      mbar_drain(done, 0);
+    }
     __syncwarp();
-    mbar_drain(done, 0);
   } else if (warp >= 4) {
-    const int q = warp & 3;
+    // Two warps per quarter of the rows, one for each half of the columns; a
+    // step is a box of 32 rows by 128 bytes.
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tempty0 = mapa_rank(tempty, 0);
+    uint8_t* box = out + (warp - 4) * C::OUT;
+    uint8_t* line = box + lane * 128;  // 16-byte piece i of a line sits at i ^ (lane & 7)
+    const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
+    const int width = f32 ? 32 : 64;  // columns of a box
     bool ok = true;
     int j = 0;
-    for (long long u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const int e = (int)(u / (TN * TK)), r = (int)(u % (TN * TK));
-      const int n = (r % TN) * 128 + q * 32 + lane, k0 = (r / TN) * C::BN;
-      const bool empty_group = p.offsets[e + 1] == p.offsets[e];
+    WUnit t;
+    while (ok && walk.take(t, teams)) {
+      if (t.k0 >= p.K) continue;
+      const int n = t.n0 + rank * 128 + q * 32, wide = 64 * t.nb, k0 = t.k0 + half * wide;
+      const bool none = t.hi == t.lo;
       const int buf = j & 1;
-      if (!empty_group) {
+      if (!none) {
         ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
       }
-      const size_t at = ((size_t)e * p.N + n) * p.K + k0;
-#pragma unroll 1
-      for (int c0 = 0; c0 < C::BN; c0 += 16) {
-        float v[16];
-        if (empty_group) {
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * wide;
+      for (int c = 0; c < wide && k0 + c < p.K && n < p.N; c += width) {
+        uint32_t v[64];  // (only 32 of fp32)
+        if (none) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] = 0.0f;
+          for (int i = 0; i < 64; ++i) v[i] = 0;
         } else {
-          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + c0, v);
+          tmem_ld32(acc + c, reinterpret_cast<float*>(v));
+          if (!f32) tmem_ld32(acc + c + 32, reinterpret_cast<float*>(v) + 32);
           tmem_wait_ld();
         }
-        if (n >= p.N) continue;
+        if (!f32) {
 #pragma unroll
-        for (int g = 0; g < 16; g += 8) {
-          // K is a multiple of 8 (16-bit) or of 4 (fp32): no partial vector
-          if (p.out_type == MOE_DT_FP32) {
-#pragma unroll
-            for (int h = 0; h < 8; h += 4)
-              if (k0 + c0 + g + h < p.K)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at + c0 + g + h) =
-                    make_float4(v[g + h], v[g + h + 1], v[g + h + 2], v[g + h + 3]);
-          } else if (k0 + c0 + g < p.K) {
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) w[h] = pack16(v[g + 2 * h], v[g + 2 * h + 1], p.out_type == MOE_DT_BF16);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw) + at + c0 + g) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 32; ++i) v[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), bf);
         }
+        tma_store_wait_read<0>();  // lane 0's store has read the box
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(line + ((i ^ (lane & 7)) * 16)) =
+              make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_3d(&tmO, box, k0 + c, n, t.e);
       }
-      if (!empty_group) {
+      if (!none) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
         ++j;
       }
     }
+    tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA leaves while the other may still signal it or read its memory
+  cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) tmem_dealloc_cg<2>(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && p.status) {
     if (*abort) atomicOr(p.status, DEV_TIMEOUT);
     if (bad) atomicOr(p.status, DEV_BAD_ROUTING);
@@ -220,11 +345,12 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const WgradParams& p0, int sms,
-                         cudaStream_t s) {
+cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to, const WgradParams& p0,
+                         int sms, cudaStream_t s) {
   WgradParams p = p0;
-  p.idesc = idesc_f16(128, WCfg::BN, p.fmt, 1, 1);
-  return launch_cluster(wgrad_kernel, sms, WCfg::THREADS, WCfg::SMEM, 1, s, ty, tx, p);
+  p.idesc = idesc_f16(WCfg::BM, 0, p.fmt, 1, 1);  // N is set tile by tile
+  return launch_cluster(wgrad_kernel, sms / 2 * 2, WCfg::THREADS,
+                        WCfg::SMEM + (p.E + 1) * sizeof(int32_t), 2, s, ty, tx, to, p);
 }
 
 }  // namespace moe
