@@ -84,12 +84,12 @@ struct Units {
 template <int BN, int BM>
 __device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off, const int* s_tile, int& e) {
   const int NT = w.NT;
-  int piece = 0, width = BN;
+  int piece = 0, cut = 0;
   if (u >= w.whole && w.cut) {
     const int i = u - w.whole;
-    piece = i & ((1 << w.cut) - 1);
-    u = w.whole + (i >> w.cut);
-    width = BN >> w.cut;
+    cut = w.cut;
+    piece = i & ((1 << cut) - 1);
+    u = w.whole + (i >> cut);
   }
   const int v = u / NT;
   while (s_tile[e + 1] <= v) ++e;
@@ -97,11 +97,22 @@ __device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off,
   const int band = local / (kBand * NT), in_band = local - band * kBand * NT;
   const int bw = min(kBand, mt - band * kBand);
   const int nt = in_band / bw, tt = band * kBand + in_band % bw;
+  // Pairs: a group's tiles have equal rows, as near as 64 divides them, so
+  // that they take equal time.  CTAs that share a group's rows and weights
+  // then stay in step and find them in the L2.
+  int width = BN, end = s_off[e + 1];
+  const int lo = s_off[e];
+  if (BM == 256) width = ((end - lo + mt - 1) / mt + 63) & ~63;
   Tile t;
   t.e = e;
   t.m0 = nt * BM;
-  t.p0 = s_off[e] + tt * BN + piece * width;
-  t.rows = min(width, s_off[e + 1] - t.p0);
+  t.p0 = lo + tt * width;
+  if (cut) {
+    end = min(end, t.p0 + width);
+    width = ((width >> cut) + 31) & ~31;
+    t.p0 += piece * width;
+  }
+  t.rows = min(width, end - t.p0);
   return t;
 }
 
