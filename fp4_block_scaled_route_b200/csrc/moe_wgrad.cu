@@ -12,26 +12,32 @@ namespace {
 // rows of 128 dy columns and of 128 x columns, in boxes of 64 columns whose
 // rows are 128-byte lines.
 //
-// Warp 0 loads, warp 1 (of the even CTA) issues the MMAs, warps 4-11 read the
-// accumulators, round them and store them by TMA from shared memory.
+// Warp 0 loads, warp 1 (of the even CTA) issues the MMAs, warp 2 zeroes what a
+// group's last stage holds past its rows, warps 4-11 read the accumulators,
+// round them and store them by TMA from shared memory.
+// Stages: 6, or 5 when the offsets of very many experts take the room.
+template <int STAGES_>
 struct WCfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int BM = 256, BN = 256;
+  static constexpr int BN = 256;
   static constexpr int CH = 64;        // rows per stage
   static constexpr int BOX = CH * 128;
   static constexpr int STAGE = 4 * BOX;  // dy: boxes 0, 1; x: boxes 2, 3
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = STAGES_;
   static constexpr int OUT = 32 * 128;  // per epilogue warp: a box of 32 rows of 128 bytes
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int BARS = 512;
   static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * OUT + BARS;  // (+ the offsets)
-  static_assert((4 * STAGES + 5) * 8 + 8 <= BARS && SMEM + kMaxGroups * 4 <= 232448, "shared memory");
+  static constexpr int MAX_E = (232448 - SMEM) / 4 - 1;
+  static_assert((4 * STAGES + 5) * 8 + 8 <= BARS && MAX_E > 0, "shared memory");
 };
 
 // Work of one pair: all features of an expert before the next column of
 // tiles, all tiles of an expert before the next expert.  The units of the
 // last, partial wave are halves of 128 columns when they still are one wave.
+constexpr int kWM = 256, kWN = 256;  // rows and columns of a tile
+
 struct WUnit {
   int e, lo, hi;  // expert, its rows
   int n0, k0, nb; // first row and column of the output, 128-column halves
@@ -41,8 +47,8 @@ struct WWalk {
   int TN, per, K, whole, halves, total;
   int u, r, e;  // next unit; its place within expert e
   __device__ __forceinline__ WWalk(const int* off, int E, int N, int K_, int team, int teams) : s_off(off), K(K_) {
-    TN = (N + WCfg::BM - 1) / WCfg::BM;
-    per = TN * ((K + WCfg::BN - 1) / WCfg::BN);
+    TN = (N + kWM - 1) / kWM;
+    per = TN * ((K + kWN - 1) / kWN);
     total = E * per;
     const int rem = total % teams;
     whole = total - rem;
@@ -68,8 +74,8 @@ struct WWalk {
     t.e = ee;
     t.lo = s_off[ee];
     t.hi = s_off[ee + 1];
-    t.n0 = (at % TN) * WCfg::BM;
-    t.k0 = (at / TN) * WCfg::BN;
+    t.n0 = (at % TN) * kWM;
+    t.k0 = (at / TN) * kWN;
     t.nb = K - t.k0 > 128 ? 2 : 1;
     if (halves && u >= whole) {
       t.nb = 1;
@@ -86,11 +92,11 @@ struct WWalk {
   }
 };
 
-__global__ void __launch_bounds__(WCfg::THREADS, 1)
+template <int STAGES>
+__global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                  const __grid_constant__ CUtensorMap tmO, const WgradParams p) {
-  using C = WCfg;
-  constexpr int STAGES = C::STAGES;
+  using C = WCfg<STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out = smem + STAGES * C::STAGE;
@@ -196,11 +202,11 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         if (armed_part & (1u << s)) mbar_drain(&part[s], ((uses >> s) & 1u) ^ 1u);
       }
     __syncwarp();
-  } else if (warp == 1) {
-    const uint32_t empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), zeroed0 = mapa_rank(zeroed, 0);
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t empty0 = smem_u32(empty), tfull0 = smem_u32(tfull);
     const uint64_t ad0 = sdesc_mn_sw128(smem_u32(smem), C::BOX);
     const uint64_t bd0 = sdesc_mn_sw128(smem_u32(smem) + 2 * C::BOX, C::BOX);
-    uint32_t uses = 0;  // parity of each stage's next use of part / zeroed
+    uint32_t uses = 0;  // parity of each stage's next use of zeroed
     uint32_t st = 0, ph = 0;
     bool ok = true;
     int j = 0;
@@ -215,50 +221,30 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
       }
       const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
       const int buf = j & 1;
-      if (rank == 0) {
-        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-        if (!ok) break;
-        tc_fence_after();
-      }
+      ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
+      if (!ok) break;
+      tc_fence_after();
       for (int row = lo; row < hi; row += C::CH) {
         const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
-        if (ragged(hi - row)) {
-          // The last step's rows past the group's end belong to the next
-          // group (or to no one) and may hold anything, NaN too: zeros in
-          // both operands.  A row is one 128-byte line of each box, whatever
-          // the swizzle does inside it.
-          uint8_t* a = smem + st * C::STAGE;
-          const uint32_t use = (uses >> st) & 1u;
+        // (a stage with a ragged tail: its bytes are counted elsewhere, and
+        // warp 2 of both CTAs says when they are in and the tail is zeroed)
+        ok = mbar_wait_warp(&full[st], ph, abort);
+        if (ok && ragged(hi - row)) {
+          ok = mbar_wait_cluster(&zeroed[st], (uses >> st) & 1u, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
           uses ^= 1u << st;
-          ok = mbar_wait_warp(&part[st], use, abort);
-          if (!ok) break;
-          const int pieces = (steps * 16 - held) * 8;
-          for (int i = lane; i < pieces * (2 + nb); i += 32)
-            *reinterpret_cast<uint4*>(a + (i / pieces) * C::BOX + held * 128 + (i % pieces) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(zeroed0 + 8u * st);
-          if (rank == 0) {
-            ok = mbar_wait_cluster(&zeroed[st], use, abort);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-          }
         }
-        if (rank == 0) {
-          ok = mbar_wait_warp(&full[st], ph, abort);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t off = st * (C::STAGE >> 4);
-          const uint32_t d = tmem + buf * C::BN;
-          if (steps == 4) {
-            mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, row != lo);
-          } else {
-            for (int kk = 0; kk < steps; ++kk)
-              mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != lo) | (kk != 0));
-          }
-          mma_commit_all<2>(empty0 + 8u * st);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t off = st * (C::STAGE >> 4);
+        const uint32_t d = tmem + buf * C::BN;
+        if (steps == 4) {
+          mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, row != lo);
+        } else {
+          for (int kk = 0; kk < steps; ++kk)
+            mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != lo) | (kk != 0));
         }
+        mma_commit_all<2>(empty0 + 8u * st);
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
@@ -266,12 +252,43 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         // the next unit is looked up while the tensor cores have work
         if (row == lo) more = walk.take(next, teams);
       }
-      if (ok && rank == 0) mma_commit_all<2>(tfull0 + 8u * buf);
+      if (ok) mma_commit_all<2>(tfull0 + 8u * buf);
       ++j;
     }
-    if (rank == 0) {
-      mma_commit_all<2>(smem_u32(done));
-      mbar_drain(done, 0);
+    mma_commit_all<2>(smem_u32(done));
+    mbar_drain(done, 0);
+    __syncwarp();
+  } else if (warp == 2) {
+    // The rows of a stage past the group's end belong to the next group (or
+    // to no one) and may hold anything, NaN too: zeros in both operands, up
+    // to the end of the last 16-row step.  A row is one 128-byte line of each
+    // box, whatever the swizzle does inside it.  Each CTA's warp 2 does so in
+    // its own shared memory, ahead of the warp that issues the MMAs: done by
+    // that warp it cost 15 % of the time at 512 rows a group.
+    const uint32_t zeroed0 = mapa_rank(zeroed, 0);
+    uint32_t uses = 0, st = 0;
+    bool ok = true;
+    WUnit t;
+    while (ok && walk.take(t, teams)) {
+      if (t.hi == t.lo || t.k0 >= p.K) continue;
+      const int rows = t.hi - t.lo, last = (rows - 1) / C::CH;
+      if (ragged(rows - last * C::CH)) {
+        const int held = rows - last * C::CH, pieces = ((held + 15) / 16 * 16 - held) * 8;
+        const uint32_t s = (st + last) % STAGES;
+        uint8_t* a = smem + s * C::STAGE;
+        ok = mbar_wait_warp(&part[s], (uses >> s) & 1u, abort);
+        if (!ok) break;
+        uses ^= 1u << s;
+        for (int i = lane; i < pieces; i += 32) {
+          uint4* at = reinterpret_cast<uint4*>(a + held * 128 + i * 16);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) at[b * (C::BOX / 16)] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(zeroed0 + 8u * s);
+      }
+      st = (st + last + 1) % STAGES;
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -283,6 +300,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
     uint8_t* line = box + lane * 128;  // 16-byte piece i of a line sits at i ^ (lane & 7)
     const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
     const int width = f32 ? 32 : 64;  // columns of a box
+    const uint64_t pol = policy_evict_normal();
     bool ok = true;
     int j = 0;
     WUnit t;
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
               make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tma_store_3d(&tmO, box, k0 + c, n, t.e);
+        if (lane == 0) tma_store_3d(&tmO, box, k0 + c, n, t.e, pol);
       }
       if (!none) {
         tc_fence_before();
@@ -348,9 +366,12 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
 cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to, const WgradParams& p0,
                          int sms, cudaStream_t s) {
   WgradParams p = p0;
-  p.idesc = idesc_f16(WCfg::BM, 0, p.fmt, 1, 1);  // N is set tile by tile
-  return launch_cluster(wgrad_kernel, sms / 2 * 2, WCfg::THREADS,
-                        WCfg::SMEM + (p.E + 1) * sizeof(int32_t), 2, s, ty, tx, to, p);
+  p.idesc = idesc_f16(kWM, 0, p.fmt, 1, 1);  // N is set tile by tile
+  const size_t table = (p.E + 1) * sizeof(int32_t);
+  static_assert(WCfg<5>::MAX_E >= 1024, "every expert count has a variant");
+  if (p.E <= WCfg<6>::MAX_E)
+    return launch_cluster(wgrad_kernel<6>, sms / 2 * 2, WCfg<6>::THREADS, WCfg<6>::SMEM + table, 2, s, ty, tx, to, p);
+  return launch_cluster(wgrad_kernel<5>, sms / 2 * 2, WCfg<5>::THREADS, WCfg<5>::SMEM + table, 2, s, ty, tx, to, p);
 }
 
 }  // namespace moe
