@@ -426,7 +426,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
                    int grid, cudaStream_t s) {
   using C = Cfg<KIND, BN, CG, SPLIT>;
   if (SPLIT && p.split > C::MAX_SPLIT) return cudaErrorInvalidValue;
-  return launch_cluster(grouped_kernel<KIND, BN, CG, SPLIT>, grid, C::THREADS, C::SMEM, SPLIT ? p.split : CG, s, tw, tx,
+  return launch_cluster<grouped_kernel<KIND, BN, CG, SPLIT>>(grid, C::THREADS, C::SMEM, SPLIT ? p.split : CG, s, tw, tx,
                         txs, p);
 }
 

@@ -69,12 +69,16 @@ bool row_stride_ok(long long ld, long long n, int es) {
 
 // The current device's SM count; MOE_ERR_UNSUPPORTED when it is no sm_100.
 moe_status device_sms(int* sms) {
+  static std::atomic<int> known[64];  // SM count of a usable device, 0: not asked yet
   int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) != 0) return MOE_OK;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return major == 10 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  if (major != 10) return MOE_ERR_UNSUPPORTED;
+  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 moe_status sizes_ok(int E, int P, int N, int K) {

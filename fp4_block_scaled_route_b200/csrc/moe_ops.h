@@ -3,6 +3,7 @@
 // translation units (not part of the public C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -108,12 +109,20 @@ cudaError_t launch_row_combine_bwd(const RowCombineBwdParams& p, int dtype, cuda
 // Launch as a programmatic dependent of the kernel before it in the stream
 // (the kernels wait, before they read anything, until that one is complete),
 // in clusters of `cluster` CTAs.
-template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
-                           cudaStream_t s, const Args&... args) {
-  if (smem > 48 * 1024) {  // the attribute belongs to the current device's context
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <auto Kernel, typename... Args>
+cudaError_t launch_cluster(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const Args&... args) {
+  if (smem > 48 * 1024) {
+    // once per kernel and device: the attribute belongs to the device's context
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+      if (e != cudaSuccess) return e;
+      done.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -129,7 +138,7 @@ cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, si
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, Kernel, args...);
 }
 
 }  // namespace moe

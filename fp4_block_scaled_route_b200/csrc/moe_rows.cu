@@ -357,32 +357,32 @@ unsigned blocks(long long n, int per) { return (unsigned)((n + per - 1) / per); 
 template <typename T>
 cudaError_t quant_int8(const QuantInt8Params& p, cudaStream_t s) {
   // the fewest warps that keep a row in registers
-  if (p.K <= 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 1>, blocks(p.rows, 8), kThreads, 0, 1, s, p);
-  else if (p.K <= 2 * 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 2>, blocks(p.rows, 4), kThreads, 0, 1, s, p);
-  else if (p.K <= 4 * 512 * kKeep) return launch_cluster(quant_int8_kernel<T, 4>, blocks(p.rows, 2), kThreads, 0, 1, s, p);
-  else return launch_cluster(quant_int8_kernel<T, 8>, p.rows, kThreads, 0, 1, s, p);
+  if (p.K <= 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 1>>(blocks(p.rows, 8), kThreads, 0, 1, s, p);
+  else if (p.K <= 2 * 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 2>>(blocks(p.rows, 4), kThreads, 0, 1, s, p);
+  else if (p.K <= 4 * 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 4>>(blocks(p.rows, 2), kThreads, 0, 1, s, p);
+  else return launch_cluster<quant_int8_kernel<T, 8>>(p.rows, kThreads, 0, 1, s, p);
 }
 
 template <typename T>
 cudaError_t row_combine(const RowCombineParams& p, cudaStream_t s) {
-  return launch_cluster(combine_kernel<T>, dim3(p.T, blocks(p.H, kThreads * Vec<T>::N)), kThreads, 0, 1, s, p);
+  return launch_cluster<combine_kernel<T>>(dim3(p.T, blocks(p.H, kThreads * Vec<T>::N)), kThreads, 0, 1, s, p);
 }
 
 template <typename T>
 cudaError_t row_combine_bwd(const RowCombineBwdParams& p, cudaStream_t s) {
   const long long slots = (long long)p.T * (p.k + p.n_shared);
   // few slots: a block each, so that a row's columns are read side by side
-  if (slots <= kFewSlots) return launch_cluster(combine_bwd_kernel<T, 8>, blocks(slots, 1), kThreads, 0, 1, s, p);
-  else return launch_cluster(combine_bwd_kernel<T, 1>, blocks(slots, 8), kThreads, 0, 1, s, p);
+  if (slots <= kFewSlots) return launch_cluster<combine_bwd_kernel<T, 8>>(blocks(slots, 1), kThreads, 0, 1, s, p);
+  else return launch_cluster<combine_bwd_kernel<T, 1>>(blocks(slots, 8), kThreads, 0, 1, s, p);
 }
 }  // namespace
 
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s) {
   if (p.row_bytes <= 512 * kCopies) {
-    return launch_cluster(permute_kernel<1>, blocks(p.rows, 8), kThreads, 0, 1, s, p);
+    return launch_cluster<permute_kernel<1>>(blocks(p.rows, 8), kThreads, 0, 1, s, p);
   } else {
     const unsigned chunks = blocks(p.row_bytes, 512 * 8 * kCopies);
-    return launch_cluster(permute_kernel<8>, dim3(p.rows, chunks < 64 ? chunks : 64), kThreads, 0, 1, s, p);
+    return launch_cluster<permute_kernel<8>>(dim3(p.rows, chunks < 64 ? chunks : 64), kThreads, 0, 1, s, p);
   }
 }
 

@@ -370,8 +370,8 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
   const size_t table = (p.E + 1) * sizeof(int32_t);
   static_assert(WCfg<5>::MAX_E >= 1024, "every expert count has a variant");
   if (p.E <= WCfg<6>::MAX_E)
-    return launch_cluster(wgrad_kernel<6>, sms / 2 * 2, WCfg<6>::THREADS, WCfg<6>::SMEM + table, 2, s, ty, tx, to, p);
-  return launch_cluster(wgrad_kernel<5>, sms / 2 * 2, WCfg<5>::THREADS, WCfg<5>::SMEM + table, 2, s, ty, tx, to, p);
+    return launch_cluster<wgrad_kernel<6>>(sms / 2 * 2, WCfg<6>::THREADS, WCfg<6>::SMEM + table, 2, s, ty, tx, to, p);
+  return launch_cluster<wgrad_kernel<5>>(sms / 2 * 2, WCfg<5>::THREADS, WCfg<5>::SMEM + table, 2, s, ty, tx, to, p);
 }
 
 }  // namespace moe

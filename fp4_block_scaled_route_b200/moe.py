@@ -401,8 +401,9 @@ class MoeLayer:
         if topk_ids.shape != (T, self.k):
             raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, {self.k}]")
         NG, P = self.E + self.n_shared, T * (self.k + self.n_shared)
-        _vector(topk_ids, P - T * self.n_shared, "route: topk_ids")
-        dev = _device("route", ("topk_ids", topk_ids, torch.int32))
+        _vector(topk_ids, P - T * self.n_shared, "route", "topk_ids")
+        dev = topk_ids.get_device()
+        _on("route", max(dev, 0), "topk_ids", topk_ids, torch.int32)
 
         def body(s):
             counts, offsets, perm, inv = (torch.empty(n, dtype=torch.int32, device=dev) for n in (NG, NG + 1, P, P))
@@ -452,101 +453,112 @@ def finalize_bf16(acc, out=None, stream=None):
 
 
 # ---- expert operators on torch tensors (marshalling only) -----------------
-def _device(what, *tensors):
-    """The one CUDA device of `tensors`, each (name, tensor or None, required dtype or None)."""
-    dev = None
-    for name, t, dtype in tensors:
-        if t is None:
-            continue
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
-        d = t.device
-        if d != dev:
-            if d.type != "cuda":
-                raise ValueError(f"{what}: {name} is not a CUDA tensor")
-            if dev is not None:
-                raise ValueError(f"{what}: {name} is on {d}, not on {dev}")
-            dev = d
-    return dev
+# Small calls are bound by the host, so the checks below are flat and build
+# their messages only when they fail.
+def _on(what, dev, name, t, dtype):
+    """Refuses t (None passes) unless it is a `dtype` tensor on CUDA device `dev`."""
+    if t is None:
+        return
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: {name} is on {t.device}, not on cuda:{dev}" if t.is_cuda else
+                         f"{what}: {name} is not a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
 
 
 def _call(what, dev, stream, body):
-    """body(stream handle) with `dev` current and `stream` (default: that device's current one) the stream that results
-    are allocated on."""
+    """body(stream handle) with device `dev` current and `stream` (default: that device's current one) the stream that
+    results are allocated on."""
     import torch
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return body(torch.cuda.current_stream(dev).cuda_stream)
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {dev}")
+    if dev < 0:
+        raise ValueError(f"{what}: the first argument is not a CUDA tensor")
+    if stream is None and torch.cuda.current_device() == dev:
+        # the handle alone: torch.cuda.current_stream() builds an object around it, 2 us
+        return body(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
-        return body(torch.cuda.current_stream(dev).cuda_stream)
+        return body(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _dtype_code(dtype, what):
     import torch
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return MOE_DT_BF16
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         return MOE_DT_FP16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return MOE_DT_FP32
     raise ValueError(f"{what}: type {dtype} is not supported")
 
 
-def _new_rows(rows, n, dtype, device):
+def _new_rows(rows, n, dtype, dev):
     """An unset [rows, n] matrix whose row stride is a multiple of 16 bytes (contiguous where n allows it)."""
     import torch
     step = 16 // dtype.itemsize
-    if n % step == 0:
-        return torch.empty((rows, n), dtype=dtype, device=device)
-    return torch.empty((rows, -(-n // step) * step), dtype=dtype, device=device)[:, :n]
+    return torch.empty_strided((rows, n), (-(-n // step) * step, 1), dtype=dtype, device=dev)
 
 
-def _matrix(t, shape, what):
-    """Row stride in elements of a matrix with contiguous rows; `shape` may hold None for any size."""
-    got = t.shape
-    if len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got)):
-        raise ValueError(f"{what} has shape {tuple(got)}, not {tuple('any' if n is None else n for n in shape)}")
-    st = t.stride()
-    if st[-1] != 1 and got[-1] > 1:
-        raise ValueError(f"{what}: rows are not contiguous")
-    if got[-2] > 1:
-        return st[-2]
+def _matrix(t, rows, cols, what, name):
+    """Row stride in elements of a [rows, cols] matrix with contiguous rows; None: any size."""
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{what}: {name} has shape {tuple(shape)}, not "
+                         f"[{'any' if rows is None else rows}, {'any' if cols is None else cols}]")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: {name}: rows are not contiguous")
+    if shape[0] > 1:
+        return s0
     step = 16 // t.element_size()      # a single row: its stride is never used
-    return -(-got[-1] // step) * step
+    return -(-shape[1] // step) * step
 
 
-def _vector(t, n, what):
+def _vector(t, n, what, name):
     if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
+        raise ValueError(f"{what}: {name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
 
 
 def _weights(w, offsets, what):
     """(E, N, K, row stride, expert stride) of the weights; offsets [E + 1] fit them."""
-    if w.dim() != 3:
-        raise ValueError(f"{what}: w has shape {tuple(w.shape)}, not [E, N, K]")
-    E, N, K = w.shape
-    if offsets is not None and (offsets.shape != (E + 1,) or not offsets.is_contiguous()):
+    shape = w.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what}: w has shape {tuple(shape)}, not [E, N, K]")
+    E, N, K = shape
+    if offsets is not None and (offsets.numel() != E + 1 or offsets.dim() != 1 or not offsets.is_contiguous()):
         raise ValueError(f"{what}: offsets has shape {tuple(offsets.shape)}, not [{E + 1}]")
-    return E, N, K, _matrix(w, (E, N, K), f"{what}: w"), (w.stride(0) if E > 1 else 0)
+    se, sn, sk = w.stride()
+    if sk != 1 and K > 1:
+        raise ValueError(f"{what}: w: rows are not contiguous")
+    step = 16 // w.element_size()
+    return E, N, K, sn if N > 1 else -(-K // step) * step, se if E > 1 else 0
 
 
-def _grouped(entry, what, name, rows, contract, w, offsets, out, out_dtype, status, stream):
+def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, status, stream):
     import torch
     E, N, K, ldw, sw = _weights(w, offsets, what)
-    R, M = (K, N) if contract == "k" else (N, K)
     P = rows.shape[0]
-    ld = _matrix(rows, (P, R), f"{what}: {name}")
+    R, M = (K, N) if forward else (N, K)
+    ld = _matrix(rows, P, R, what, name)
     dtype = rows.dtype
-    out_dtype = out.dtype if out is not None else (out_dtype or dtype)
-    dt, odt = _dtype_code(dtype, what), _dtype_code(out_dtype, what)
-    dev = _device(what, (name, rows, None), ("w", w, dtype), ("offsets", offsets, torch.int32), ("out", out, None),
-                  ("status", status, torch.int32))
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = dtype
+    dt = _dtype_code(dtype, what)
+    odt = dt if out_dtype is dtype else _dtype_code(out_dtype, what)
+    dev = rows.get_device()
+    _on(what, max(dev, 0), name, rows, dtype)
+    _on(what, dev, "w", w, dtype)
+    _on(what, dev, "offsets", offsets, torch.int32)
+    _on(what, dev, "out", out, out_dtype)
+    _on(what, dev, "status", status, torch.int32)
 
     def body(s):
         y = _new_rows(P, M, out_dtype, dev) if out is None else out
-        _check(entry(dt, odt, E, P, N, K, _ptr(offsets), _ptr(rows), ld, _ptr(w), ldw, sw, _ptr(y),
-                     _matrix(y, (P, M), f"{what}: out"), _ptr(status), s), entry.__name__)
+        ldy = _matrix(y, P, M, what, "out")
+        _check(entry(dt, odt, E, P, N, K, offsets.data_ptr(), rows.data_ptr(), ld, w.data_ptr(), ldw, sw, y.data_ptr(),
+                     ldy, _ptr(status), s), entry.__name__)
         return y
     return _call(what, dev, stream, body)
 
@@ -557,12 +569,12 @@ def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=No
     x [P, K] and w [E, N, K] bf16 or fp16 with contiguous rows (any row and expert strides that are multiples of 16
     bytes), offsets device int32 [E+1]; out [P, N] in the same type or fp32.  Rows outside every group are left as
     they were (unspecified in an `out` made here).  status: optional device int32, see moe.h."""
-    return _grouped(moe_grouped_gemm, "grouped_gemm", "x", x, "k", w, offsets, out, out_dtype, status, stream)
+    return _grouped(moe_grouped_gemm, "grouped_gemm", "x", x, True, w, offsets, out, out_dtype, status, stream)
 
 
 def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, status=None, stream=None):
     """dx[p] = dy[p] w[e], the gradient of grouped_gemm for x (moe_grouped_gemm_dgrad): dy [P, N] -> [P, K]."""
-    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", "dy", dy, "n", w, offsets, out, out_dtype, status,
+    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", "dy", dy, False, w, offsets, out, out_dtype, status,
                     stream)
 
 
@@ -571,15 +583,19 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
     dy [P, N], x [P, K] -> [E, N, K], zeros for an expert without rows."""
     import torch
     what = "grouped_gemm_wgrad"
-    lddy = _matrix(dy, (None, None), f"{what}: dy")
-    ldx = _matrix(x, (dy.shape[0], None), f"{what}: x")
+    lddy = _matrix(dy, None, None, what, "dy")
+    ldx = _matrix(x, dy.shape[0], None, what, "x")
     (P, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
-    _vector(offsets, E + 1, f"{what}: offsets")
+    _vector(offsets, E + 1, what, "offsets")
     dtype = dy.dtype
     out_dtype = out.dtype if out is not None else (out_dtype or dtype)
     dt, odt = _dtype_code(dtype, what), _dtype_code(out_dtype, what)
-    dev = _device(what, ("dy", dy, None), ("x", x, dtype), ("offsets", offsets, torch.int32), ("out", out, None),
-                  ("status", status, torch.int32))
+    dev = dy.get_device()
+    _on(what, max(dev, 0), "dy", dy, dy.dtype)
+    _on(what, dev, "x", x, dtype)
+    _on(what, dev, "offsets", offsets, torch.int32)
+    _on(what, dev, "out", out, out_dtype)
+    _on(what, dev, "status", status, torch.int32)
     if out is not None and (out.shape != (E, N, K) or not out.is_contiguous()):
         raise ValueError(f"{what}: out is not contiguous [{E}, {N}, {K}]")
 
@@ -596,21 +612,24 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
     With perm (device int32 [rows]) row p is token perm[p] // k, quantised in expert order."""
     import torch
     what = "quant_int8"
-    ldx = _matrix(x, (None, None), f"{what}: x")
+    ldx = _matrix(x, None, None, what, "x")
     T, K = x.shape
     rows = T if perm is None else perm.shape[0]
     dt = _dtype_code(x.dtype, what)
-    dev = _device(what, ("x", x, None), ("perm", perm, torch.int32), ("out", out, torch.int8),
-                  ("scale", scale, torch.float32))
+    dev = x.get_device()
+    _on(what, max(dev, 0), "x", x, x.dtype)
+    _on(what, dev, "perm", perm, torch.int32)
+    _on(what, dev, "out", out, torch.int8)
+    _on(what, dev, "scale", scale, torch.float32)
     if perm is not None:
-        _vector(perm, rows, f"{what}: perm")
+        _vector(perm, rows, what, "perm")
 
     def body(s):
         q = _new_rows(rows, K, torch.int8, dev) if out is None else out
-        sc = torch.empty(rows, dtype=torch.float32, device=dev) if scale is None else scale
-        _vector(sc, rows, f"{what}: scale")
+        sc = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=dev) if scale is None else scale
+        _vector(sc, rows, what, "scale")
         _check(moe_quant_int8(dt, rows, K, T, k, _ptr(x), ldx, _ptr(perm), _ptr(q),
-                              _matrix(q, (rows, K), f"{what}: out"), _ptr(sc), s), "moe_quant_int8")
+                              _matrix(q, rows, K, what, "out"), _ptr(sc), s), "moe_quant_int8")
         return q, sc
     return _call(what, dev, stream, body)
 
@@ -622,26 +641,32 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
     dense product), offsets device int32 [E+1].  out [P, N] bf16 (default), fp16 or fp32."""
     import torch
     what = "int8_gemm"
-    if offsets is None:
-        if w.dim() == 2:
-            w = w[None]
-        if w.dim() != 3 or w.shape[0] != 1:
-            raise ValueError(f"{what}: w has shape {tuple(w.shape)}; one matrix without offsets, [E, N, K] with them")
-    E, N, K, ldw, sw = _weights(w, offsets, what)
+    if offsets is None and w.dim() == 2:
+        (N, K), E, sw = w.shape, 1, 0
+        ldw = _matrix(w, N, K, what, "w")
+    elif offsets is None and (w.dim() != 3 or w.shape[0] != 1):
+        raise ValueError(f"{what}: w has shape {tuple(w.shape)}; one matrix without offsets, [E, N, K] with them")
+    else:
+        E, N, K, ldw, sw = _weights(w, offsets, what)
     P = q.shape[0]
-    ldq = _matrix(q, (P, K), f"{what}: q")
-    _vector(q_scale, P, f"{what}: q_scale")
-    _vector(w_scale, E * N, f"{what}: w_scale")
+    ldq = _matrix(q, P, K, what, "q")
+    _vector(q_scale, P, what, "q_scale")
+    _vector(w_scale, E * N, what, "w_scale")
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     odt = _dtype_code(out_dtype, what)
-    dev = _device(what, ("q", q, torch.int8), ("q_scale", q_scale, torch.float32), ("w", w, torch.int8),
-                  ("w_scale", w_scale, torch.float32), ("offsets", offsets, torch.int32), ("out", out, None),
-                  ("status", status, torch.int32))
+    dev = q.get_device()
+    _on(what, max(dev, 0), "q", q, torch.int8)
+    _on(what, dev, "q_scale", q_scale, torch.float32)
+    _on(what, dev, "w", w, torch.int8)
+    _on(what, dev, "w_scale", w_scale, torch.float32)
+    _on(what, dev, "offsets", offsets, torch.int32)
+    _on(what, dev, "out", out, out_dtype)
+    _on(what, dev, "status", status, torch.int32)
 
     def body(s):
         y = _new_rows(P, N, out_dtype, dev) if out is None else out
         _check(moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), _ptr(q), ldq, _ptr(q_scale), _ptr(w), ldw, sw,
-                             _ptr(w_scale), _ptr(y), _matrix(y, (P, N), f"{what}: out"), _ptr(status), s),
+                             _ptr(w_scale), _ptr(y), _matrix(y, P, N, what, "out"), _ptr(status), s),
                "moe_int8_gemm")
         return y
     return _call(what, dev, stream, body)
@@ -652,17 +677,20 @@ def permute(x, perm, k, out=None, stream=None):
     -1 are left as they were (unspecified in an `out` made here)."""
     import torch
     what = "permute"
-    ldx = _matrix(x, (None, None), f"{what}: x")
+    ldx = _matrix(x, None, None, what, "x")
     T, H = x.shape
     rows = perm.shape[0]
-    _vector(perm, rows, f"{what}: perm")
+    _vector(perm, rows, what, "perm")
     dt = _dtype_code(x.dtype, what)
-    dev = _device(what, ("x", x, None), ("perm", perm, torch.int32), ("out", out, x.dtype))
+    dev = x.get_device()
+    _on(what, max(dev, 0), "x", x, x.dtype)
+    _on(what, dev, "perm", perm, torch.int32)
+    _on(what, dev, "out", out, x.dtype)
 
     def body(s):
         y = _new_rows(rows, H, x.dtype, dev) if out is None else out
         _check(moe_permute(dt, rows, H, T, k, _ptr(x), ldx, _ptr(perm), _ptr(y),
-                           _matrix(y, (rows, H), f"{what}: out"), s), "moe_permute")
+                           _matrix(y, rows, H, what, "out"), s), "moe_permute")
         return y
     return _call(what, dev, stream, body)
 
@@ -673,12 +701,12 @@ def _combine_sizes(inv, topk_w, k, n_shared, what):
         if topk_w.dim() != 2 or (k is not None and topk_w.shape[1] != k):
             raise ValueError(f"{what}: topk_w has shape {tuple(topk_w.shape)}, not [T, k]")
         T, k = topk_w.shape
-        _vector(topk_w, T * k, f"{what}: topk_w")
+        _vector(topk_w, T * k, what, "topk_w")
     else:
         if k is None:
             raise ValueError(f"{what}: without topk_w, k has to be given")
         T = inv.numel() // (k + n_shared)
-    _vector(inv, T * (k + n_shared), f"{what}: inv")
+    _vector(inv, T * (k + n_shared), what, "inv")
     return T, k
 
 
@@ -687,17 +715,20 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
     topk_w fp32 [T, k], or None (ones; then k is given): the gradient of permute."""
     import torch
     what = "combine"
-    ldy = _matrix(y, (None, None), f"{what}: y")
+    ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
     T, k = _combine_sizes(inv, topk_w, k, n_shared, what)
     dt = _dtype_code(y.dtype, what)
-    dev = _device(what, ("y", y, None), ("inv", inv, torch.int32), ("topk_w", topk_w, torch.float32),
-                  ("out", out, y.dtype))
+    dev = y.get_device()
+    _on(what, max(dev, 0), "y", y, y.dtype)
+    _on(what, dev, "inv", inv, torch.int32)
+    _on(what, dev, "topk_w", topk_w, torch.float32)
+    _on(what, dev, "out", out, y.dtype)
 
     def body(s):
         o = _new_rows(T, H, y.dtype, dev) if out is None else out
         _check(moe_combine(dt, rows, H, T, k, n_shared, _ptr(y), ldy, _ptr(inv), _ptr(topk_w), _ptr(o),
-                           _matrix(o, (T, H), f"{what}: out"), s), "moe_combine")
+                           _matrix(o, T, H, what, "out"), s), "moe_combine")
         return o
     return _call(what, dev, stream, body)
 
@@ -708,19 +739,24 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     import torch
     what = "combine_backward"
     T, k = _combine_sizes(inv, topk_w, None, n_shared, what)
-    ldy = _matrix(y, (None, None), f"{what}: y")
+    ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
-    ldd = _matrix(dout, (T, H), f"{what}: dout")
+    ldd = _matrix(dout, T, H, what, "dout")
     dt = _dtype_code(y.dtype, what)
-    dev = _device(what, ("y", y, None), ("dout", dout, y.dtype), ("inv", inv, torch.int32),
-                  ("topk_w", topk_w, torch.float32), ("dy", dy, y.dtype), ("dtopk_w", dtopk_w, torch.float32))
+    dev = y.get_device()
+    _on(what, max(dev, 0), "y", y, y.dtype)
+    _on(what, dev, "dout", dout, y.dtype)
+    _on(what, dev, "inv", inv, torch.int32)
+    _on(what, dev, "topk_w", topk_w, torch.float32)
+    _on(what, dev, "dy", dy, y.dtype)
+    _on(what, dev, "dtopk_w", dtopk_w, torch.float32)
 
     def body(s):
         gy = _new_rows(rows, H, y.dtype, dev) if dy is None else dy
-        gw = torch.empty((T, k), dtype=torch.float32, device=dev) if dtopk_w is None else dtopk_w
-        _vector(gw, T * k, f"{what}: dtopk_w")
+        gw = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=dev) if dtopk_w is None else dtopk_w
+        _vector(gw, T * k, what, "dtopk_w")
         _check(moe_combine_backward(dt, rows, H, T, k, n_shared, _ptr(dout), ldd, _ptr(y), ldy, _ptr(inv),
-                                    _ptr(topk_w), _ptr(gy), _matrix(gy, (rows, H), f"{what}: dy"), _ptr(gw), s),
+                                    _ptr(topk_w), _ptr(gy), _matrix(gy, rows, H, what, "dy"), _ptr(gw), s),
                "moe_combine_backward")
         return gy, gw
     return _call(what, dev, stream, body)
