@@ -36,7 +36,7 @@ struct Cfg {
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int SMEM = 1024 + STAGES * STAGE + TABLE + BARS + TURN + JOIN;
   static constexpr int BOX = 32;  // rows of a small box (pairs: tiles that are not full)
-  static_assert((2 * STAGES + 6) * 8 + 8 <= BARS, "barriers");
+  static_assert((2 * STAGES + 13) * 8 + 8 + 16 <= BARS, "barriers");
   static_assert(BN % (16 * CG) == 0 && BN <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile");
   static_assert(!SPLIT || CG == 1, "clusters either pair up or share a contraction");
   static_assert(B_BYTES % 1024 == 0, "128-byte swizzle atoms");
@@ -49,6 +49,12 @@ constexpr int kBand = 8;
 
 // Contraction steps (128 bytes each) that a share of a split tile keeps.
 constexpr int kMinChunks = 4;
+
+// Units are handed out at run time from this many contraction steps on, when
+// there are several groups; a pair asks for its next unit kAhead steps before
+// it is through loading the present one.
+constexpr int kHandOutChunks = 32;
+constexpr int kAhead = 12;
 
 struct Tile {
   int e, m0, p0, rows;
@@ -133,13 +139,22 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   uint64_t* tempty = tfull + 2;      // (even CTA) the epilogue warps of each CTA
   uint64_t* joined = tempty + 2;     // (SPLIT, first CTA) the other CTAs' epilogue warps
   uint64_t* done = joined + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  // Units handed out in order (p.hand_out; see warp 2):
+  uint64_t* handed = done + 1;   // [2] the next unit is in unit[] (each CTA)
+  uint64_t* taken = handed + 2;  // [2] (even CTA) every reader of both CTAs has read it
+  uint64_t* want = taken + 2;    // (even CTA) the producer nears the end of its unit
+  uint64_t* answered = want + 1; // (even CTA) the hardware's answer is in
+  volatile int* unit = reinterpret_cast<volatile int*>(answered + 1);  // [2]
+  uint8_t* answer = reinterpret_cast<uint8_t*>(full) + C::BARS - 16;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(answered + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 || SPLIT ? cluster_rank() : 0;
   const int split = SPLIT ? p.split : 1, size = CG * split;  // CTAs that work on a tile
-  const int team = blockIdx.x / size, teams = gridDim.x / size;
+  // handed-out units: the grid has a cluster per unit, and p.teams run at once
+  const bool hand_out = CG == 2 && p.hand_out;
+  const int team = blockIdx.x / size, teams = hand_out ? p.teams : gridDim.x / size;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -151,6 +166,14 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     }
     if (SPLIT) mbar_init(joined, (split - 1) * C::EPI_WARPS);
     mbar_init(done, 1);
+    if (CG == 2) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&handed[b], 1);
+        mbar_init(&taken[b], 2 * (C::EPI_WARPS + 1) + 1);
+      }
+      mbar_init(want, 1);
+      mbar_init(answered, 1);
+    }
     *abort = 0;
     mbar_fence_init();
     tma_prefetch_map(&tmW);
@@ -174,6 +197,20 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   const int kb0 = SPLIT ? (int)((long long)chunks * rank / split) : 0;
   const int kb1 = SPLIT ? (int)((long long)chunks * (rank + 1) / split) : chunks;
 
+  // The unit after u, for each warp that walks the units.
+  const uint32_t taken0 = CG == 2 ? mapa_rank(taken, 0) : 0;
+  int hand = 0;
+  auto next_unit = [&](int u) {
+    if (!hand_out) return u + teams;
+    const int b = hand & 1;
+    const bool in = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&handed[b], (uint32_t)(hand >> 1) & 1u, abort));
+    const int v = in ? unit[b] : work.total;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(taken0 + 8u * b);
+    ++hand;
+    return v;
+  };
+
   if (warp == 0) {
     const uint64_t pol_w = p.stream_w ? policy_evict_first() : policy_evict_normal();
     const uint64_t pol_x = policy_evict_normal();
@@ -181,9 +218,12 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     uint32_t armed = 0, st = 0, ph = 0;
     bool ok = true;
     int e = 0;
-    for (int u = team; u < work.total && ok; u += teams) {
+    for (int u = team; u < work.total && ok; u = next_unit(u)) {
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
-      if (t.rows <= 0) continue;
+      if (t.rows <= 0) {
+        if (hand_out && rank == 0 && lane == 0) mbar_arrive(want);
+        continue;
+      }
       // the MMA covers the tile's rows rounded up; each CTA of a pair
       // holds half of them, in small boxes unless the tile is full
       const int n = CG == 2 ? (t.rows + 31) & ~31 : BN;
@@ -194,6 +234,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = mbar_wait_warp(&empty[st], ph ^ 1u, abort);
         if (!ok) break;
+        if (hand_out && rank == 0 && lane == 0 && kb == max(kb1 - kAhead, kb0)) mbar_arrive(want);
         uint8_t* a = smem + st * C::STAGE;
         const int r0 = kb * C::CH;
         if (elect_one()) {
@@ -248,8 +289,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
       if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       while (u < work.total && ok) {
         const Tile t = next;
-        u += teams;
+        if (!hand_out) u += teams;
         if (t.rows <= 0) {
+          if (hand_out) u = next_unit(u);
           if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
           continue;
         }
@@ -271,13 +313,63 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
             ph ^= 1u;
           }
           // the next tile is looked up while the tensor cores have work
-          if (kb == kb0 && u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+          if (!hand_out && kb == kb0 && u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
         }
         if (ok) mma_commit_all<CG>(tfull0 + 8u * buf);
+        if (hand_out) {
+          u = next_unit(u);
+          if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+        }
         ++j;
       }
       mma_commit_all<CG>(smem_u32(done));
       mbar_drain(done, 0);
+    }
+    __syncwarp();
+  } else if (CG == 2 && warp == 2) {
+    // Pairs that share rows or weights find them in the L2 only while they run
+    // in step.  With units dealt out beforehand the pairs drift apart over the
+    // many tiles of ragged groups; here each pair takes the next unit just
+    // before it needs it, so that neighbours in order are neighbours in time.
+    // The even CTA's warp 2 asks the hardware and tells both CTAs.
+    if (hand_out && rank == 0 && team < work.total) {
+      const uint32_t handed0 = mapa_rank(handed, 0), handed1 = mapa_rank(handed, 1);
+      const uint32_t unit1 = mapa_rank(const_cast<const int*>(unit), 1);
+      int asked = 0;
+      bool left = true;
+      auto ask = [&](int* v) {  // the next unit's number, or none left (false)
+        if (lane == 0) {
+          mbar_arrive_expect_tx(answered, 16);
+          try_cancel(answer, answered);
+        }
+        __syncwarp();
+        const bool in = mbar_wait_warp(answered, (uint32_t)asked++ & 1u, abort);
+        const int block = in ? cancelled_block(answer) : -1;
+        fence_proxy_async_smem();  // the answer is read before the next one may land on it
+        __syncwarp();
+        *v = block >= 0 ? block / 2 : work.total;
+        return block >= 0;
+      };
+      for (int i = 0;; ++i) {
+        const int b = i & 1;
+        if (!mbar_wait_warp(want, (uint32_t)i & 1u, abort) ||
+            !mbar_wait_warp(&taken[b], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort))
+          break;
+        int v = work.total;
+        if (left) left = ask(&v);
+        if (lane == 0) {
+          unit[b] = v;
+          asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(unit1 + 4u * b), "r"(v) : "memory");
+          mbar_arrive_at(handed0 + 8u * b);
+          mbar_arrive_at(handed1 + 8u * b);
+        }
+        __syncwarp();
+        if (v >= work.total) break;
+      }
+      // the clusters past the last unit need not start at all
+      for (int v; left;) left = ask(&v);
+      // (an answer still on its way lands before the CTA leaves)
+      if (*abort && asked) mbar_drain(answered, (uint32_t)(asked - 1) & 1u);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -293,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     const uint32_t turn_st = smem_u32(turn) + (lane & 7) * 80 + (lane >> 3) * 16;
     bool ok = true;
     int j = 0, e = 0;
-    for (int u = team; u < work.total && ok; u += teams) {
+    for (int u = team; u < work.total && ok; u = next_unit(u)) {
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       if (t.rows <= 0) continue;
       const int buf = j & 1;
@@ -436,10 +528,14 @@ GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
   // Rows a tile should hold: the group's when there is one, else twice the
   // average, since routed groups vary.
   const long long want = p.E == 1 ? p.P : 2LL * ((p.P + p.E - 1) / p.E);
-  GroupedTile t{want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 256, 1, 1, sms};
+  GroupedTile t{want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 256, 1, 1, sms, sms};
   if (t.rows == 256) {
     t.ctas = 2;
-    t.grid = sms / 2 * 2;
+    t.grid = t.running = sms / 2 * 2;
+    const int steps = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
+    // a cluster for every unit there can be: tiles, and the pieces of the last wave
+    const long long units = ((p.E < p.P ? p.E : p.P) + p.P / 256) * (long long)((p.M + 255) / 256) + sms / 2;
+    if (p.E > 1 && steps >= kHandOutChunks && units * 2 < (1LL << 30)) t.grid = (int)units * 2;
     return t;
   }
   // Few tiles (at most one per group with rows, and one per full tile): share
@@ -476,6 +572,8 @@ cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const
                            const CUtensorMap& txs, const GroupedParams& p0, cudaStream_t s) {
   GroupedParams p = p0;
   p.split = t.split;
+  p.hand_out = t.ctas == 2 && t.grid > t.running;
+  p.teams = t.running / t.ctas;
   // N is set tile by tile
   p.idesc = kind == GG_INT8 ? idesc_s8(128 * t.ctas, 0) : idesc_f16(128 * t.ctas, 0, p.fmt, kind == GG_DGRAD, 0);
   if (kind == GG_FWD) return launch_kind<GG_FWD>(t, tw, tx, txs, p, s);

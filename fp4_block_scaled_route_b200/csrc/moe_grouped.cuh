@@ -283,6 +283,32 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, ui
                : "memory");
 }
 
+// ---- work handed out by the hardware --------------------------------------------
+// A grid larger than the machine has clusters that wait for room.  try_cancel
+// takes the first of them off the grid; the taker does its work instead.  The
+// answer (16 bytes) lands in shared memory and is counted on `bar`.
+__device__ __forceinline__ void try_cancel(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// First block of the cluster that was taken, or -1: none was left.
+__device__ __forceinline__ int cancelled_block(const void* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, h;\n\t}\n"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? (int)x : -1;
+}
+
 // ---- groups --------------------------------------------------------------------
 // Builds in shared memory the groups' offsets and the first row tile of each
 // group (tiles of `tile_rows` rows).  All THREADS threads of the CTA call it;

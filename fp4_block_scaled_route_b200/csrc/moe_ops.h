@@ -30,6 +30,7 @@ struct GroupedParams {
   int stream_w;             // weights are read about once: leave the L2 to the rows
   uint32_t idesc;
   int split;                // CTAs that share a tile's contraction
+  int hand_out, teams;      // pairs: units are handed out at run time to so many pairs
 };
 
 struct WgradParams {
@@ -90,10 +91,10 @@ struct RowCombineBwdParams {
 };
 
 // How a call is tiled: rows of one tile (the rows side of the MMA), CTAs of
-// one MMA, CTAs that share a tile's contraction, CTAs in all.  tx has boxes
+// one MMA, CTAs that share a tile's contraction, CTAs in all and at one time.  tx has boxes
 // of rows / ctas rows; txs, of 32, is used by pairs only.
 struct GroupedTile {
-  int rows, ctas, split, grid;
+  int rows, ctas, split, grid, running;
 };
 GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms);
 cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,

@@ -66,7 +66,6 @@ struct Vec {
 };
 
 constexpr int kThreads = 256;
-constexpr int kFewSlots = 1184;  // 8 blocks on each of 148 SMs
 
 // ---- permute: y[p] = x[token(p)] ------------------------------------------------
 // W warps copy a row, each thread up to kCopies pieces of 16 bytes that are
@@ -182,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParam
 }
 
 // ---- its gradients: W warps per slot ----------------------------------------------
+constexpr int kPieces = 4;  // pieces of 16 bytes that a thread has in flight
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const RowCombineBwdParams p) {
   griddep_wait();
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const RowCombineB
       const float g = routed ? p.g[slot] : 1.0f;
       const T* y = static_cast<const T*>(p.y) + pos * p.ldy;
       T* dy = static_cast<T*>(p.dy) + pos * p.lddy;
-      constexpr int U = 4, N = Vec<T>::N, STEP = 32 * W * N;
+      constexpr int U = kPieces, N = Vec<T>::N, STEP = 32 * W * N;
       for (int c0 = ((warp % W) * 32 + lane) * N; c0 < p.H; c0 += U * STEP) {
         Raw<T> v[U];
         Vec<T> d[U];
@@ -371,9 +371,12 @@ cudaError_t row_combine(const RowCombineParams& p, cudaStream_t s) {
 template <typename T>
 cudaError_t row_combine_bwd(const RowCombineBwdParams& p, cudaStream_t s) {
   const long long slots = (long long)p.T * (p.k + p.n_shared);
-  // few slots: a block each, so that a row's columns are read side by side
-  if (slots <= kFewSlots) return launch_cluster<combine_bwd_kernel<T, 8>>(blocks(slots, 1), kThreads, 0, 1, s, p);
-  else return launch_cluster<combine_bwd_kernel<T, 1>>(blocks(slots, 8), kThreads, 0, 1, s, p);
+  // the fewest warps that load a row's pieces all at once
+  constexpr int piece = 32 * Vec<T>::N * kPieces;
+  if (p.H <= piece) return launch_cluster<combine_bwd_kernel<T, 1>>(blocks(slots, 8), kThreads, 0, 1, s, p);
+  if (p.H <= 2 * piece) return launch_cluster<combine_bwd_kernel<T, 2>>(blocks(slots, 4), kThreads, 0, 1, s, p);
+  if (p.H <= 4 * piece) return launch_cluster<combine_bwd_kernel<T, 4>>(blocks(slots, 2), kThreads, 0, 1, s, p);
+  return launch_cluster<combine_bwd_kernel<T, 8>>(blocks(slots, 1), kThreads, 0, 1, s, p);
 }
 }  // namespace
 
