@@ -399,6 +399,12 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
           cs[i] = m < p.M ? __ldg(p.col_scale + (size_t)t.e * p.M + m) : 0.0f;
         }
       }
+      // int8: a lane holds the scale of one of the step's rows, the next
+      // step's loaded a step ahead
+      auto scale_of = [&](int c) {
+        return KIND == GG_INT8 && lane < C::CB && c + lane < t.rows ? __ldg(p.row_scale + t.p0 + c + lane) : 0.0f;
+      };
+      float next_scale = scale_of(half * C::CB);
       ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
@@ -440,6 +446,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
             }
           }
         }
+        const float row_scale = next_scale;
+        next_scale = scale_of(c0 + 2 * C::CB);
         const bool bf = p.out_type == MOE_DT_BF16;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -447,10 +455,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
           float rs[2];
           if (KIND == GG_INT8) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = i * 8 + (lane & 3) * 2 + h;
-              rs[h] = c < left ? __ldg(p.row_scale + t.p0 + c0 + c) : 0.0f;
-            }
+            for (int h = 0; h < 2; ++h) rs[h] = __shfl_sync(0xFFFFFFFFu, row_scale, i * 8 + (lane & 3) * 2 + h);
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {  // features 8 g .. 8 g + 7 of the warp's 32
