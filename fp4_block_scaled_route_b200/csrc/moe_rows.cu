@@ -229,18 +229,17 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const RowCombineB
 }
 
 // ---- row quantisation ---------------------------------------------------------------
-// 16 consecutive 16-bit values of a row, zeros past its end.
+// 8 consecutive 16-bit values of a row, zeros past its end.
+constexpr int kChunk = 8;
 struct Chunk {
-  uint32_t w[8];
+  uint32_t w[4];
   __device__ __forceinline__ void load(const uint16_t* row, int c, int n) {
-    if (c + 16 <= n) {
+    if (c + kChunk <= n) {
       const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + c));
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(row + c) + 1);
       w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const uint32_t lo = c + 2 * i < n ? row[c + 2 * i] : 0, hi = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0;
         w[i] = lo | hi << 16;
       }
@@ -248,23 +247,35 @@ struct Chunk {
   }
 };
 
-// The code of v * pre for a row maximum amax (both scaled by pre, a power of
-// two): rint(127 v / amax), ties to even.  fma(v, 127 / amax, 1.5 * 2^23)
-// leaves the rounded product in the low bits; the product is within 127 *
-// 1.5 * 2^-23 < 2.4e-5 of the quotient, so only a value that close to a tie
-// can be rounded to the wrong side, and those (1e-4 is tested) divide.  127 v
-// is exact for a 16-bit type, so the quotient's ties are seen as ties.
-__device__ __forceinline__ uint32_t code_int8(float v, float inv, float amax) {
-  const float magic = 12582912.0f;
-  float t = __fmaf_rn(v, inv, magic);
-  const float d = __fmaf_rn(v, inv, magic - t);
-  if (fabsf(d) > 0.4999f) t = rintf(__fdiv_rn(v * 127.0f, amax)) + magic;
-  return __float_as_uint(t) & 0xFFu;
+// Codes of a chunk's values v of a row with maximum amax: rint(127 v / amax),
+// ties to even.  All of it is moved by a power of two, pre, where 127 v or 1 /
+// amax would leave fp32's range: scale = 127 pre, top = amax pre, rcp = 1 / top.
+// 127 v is exact for a 16-bit type; the first quotient is off by at most 2
+// units in the last place, and its remainder brings it to within one.  A tie n + 1/2 is
+// a float, so a quotient that is one comes out exactly and rounds to even; any
+// other is at least 16 times that error away from one (a maximum of 11 bits).
+// Dividing value by value made the kernel twice as slow as its traffic (B200,
+// 8192 x 7168 bf16: 54 us).
+template <typename T>
+__device__ __forceinline__ void codes_int8(const Chunk& v, float scale, float top, float rcp, uint32_t (&o)[2]) {
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t raw = (uint16_t)(v.w[i / 2] >> (16 * (i & 1)));
+    const float f = Elem<T>::get(*reinterpret_cast<const T*>(&raw)) * scale;
+    const float q = f * rcp;
+    // adding 1.5 * 2^23 rounds to an integer and leaves it in the low byte
+    t[i] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, top, f), rcp, q), 12582912.0f));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    o[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040),
+                       0x5410);
 }
 
 // W warps per row; a thread keeps its first kKeep chunks between the two
 // passes and reads the others again.
-constexpr int kKeep = 2;
+constexpr int kKeep = 4;
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) quant_int8_kernel(const QuantInt8Params p) {
   griddep_wait();
@@ -281,17 +292,17 @@ __global__ void __launch_bounds__(kThreads) quant_int8_kernel(const QuantInt8Par
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
-    if ((i0 + k * 32 * W) * 16 < K) keep[k].load(x, (i0 + k * 32 * W) * 16, K);
+    if ((i0 + k * 32 * W) * kChunk < K) keep[k].load(x, (i0 + k * 32 * W) * kChunk, K);
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
-    if ((i0 + k * 32 * W) * 16 < K)
+    if ((i0 + k * 32 * W) * kChunk < K)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = __vmaxu2(top, keep[k].w[i] & 0x7FFF7FFFu);
-  for (int c = (i0 + kKeep * 32 * W) * 16; c < K; c += 32 * W * 16) {
+      for (int i = 0; i < 4; ++i) top = __vmaxu2(top, keep[k].w[i] & 0x7FFF7FFFu);
+  for (int c = (i0 + kKeep * 32 * W) * kChunk; c < K; c += 32 * W * kChunk) {
     Chunk v;
     v.load(x, c, K);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v.w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v.w[i] & 0x7FFF7FFFu);
   }
   top = max(top & 0xFFFFu, top >> 16);
   top = __reduce_max_sync(0xFFFFFFFFu, top);
@@ -305,35 +316,26 @@ __global__ void __launch_bounds__(kThreads) quant_int8_kernel(const QuantInt8Par
   const bool finite = top < (bf ? 0x7F80u : 0x7C00u);
   const uint16_t top16 = (uint16_t)top;
   const float amax = Elem<T>::get(*reinterpret_cast<const T*>(&top16));
-  // near the ends of bf16's range 127 v or 127 / amax leaves fp32's: move the row by 2^64
-  const float pre = !finite || amax == 0.0f ? 0.0f : amax > 1e30f ? 0x1p-64f : amax < 1e-30f ? 0x1p64f : 1.0f;
-  const float top_pre = amax * pre, inv = pre == 0.0f ? 0.0f : __fdiv_rn(127.0f, top_pre);
+  // near the ends of bf16's range 127 v leaves fp32's: such rows are moved by 2^64
+  const float pre = amax > 1e30f ? 0x1p-64f : amax < 1e-30f ? 0x1p64f : 1.0f;
+  const bool zero = !finite || amax == 0.0f;
+  const float rcp = zero ? 0.0f : __fdiv_rn(1.0f, amax * pre);
   int8_t* q = p.q + pos * p.ldq;
   auto put = [&](const Chunk& v, int c) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t b = 0;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint16_t raw = (uint16_t)(v.w[2 * i + h / 2] >> (16 * (h & 1)));
-        const float f = Elem<T>::get(*reinterpret_cast<const T*>(&raw));
-        b |= (pre == 0.0f ? 0u : code_int8(pre == 1.0f ? f : f * pre, inv, top_pre)) << (8 * h);
-      }
-      o[i] = b;
-    }
-    if (c + 16 <= K) {
-      *reinterpret_cast<uint4*>(q + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    uint32_t o[2] = {0, 0};
+    if (!zero) codes_int8<T>(v, 127.0f * pre, amax * pre, rcp, o);
+    if (c + kChunk <= K) {
+      *reinterpret_cast<uint2*>(q + c) = make_uint2(o[0], o[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < kChunk; ++i)
         if (c + i < K) q[c + i] = (int8_t)(o[i / 4] >> (8 * (i & 3)));
     }
   };
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
-    if ((i0 + k * 32 * W) * 16 < K) put(keep[k], (i0 + k * 32 * W) * 16);
-  for (int c = (i0 + kKeep * 32 * W) * 16; c < K; c += 32 * W * 16) {
+    if ((i0 + k * 32 * W) * kChunk < K) put(keep[k], (i0 + k * 32 * W) * kChunk);
+  for (int c = (i0 + kKeep * 32 * W) * kChunk; c < K; c += 32 * W * kChunk) {
     Chunk v;
     v.load(x, c, K);
     put(v, c);
@@ -349,9 +351,9 @@ unsigned blocks(long long n, int per) { return (unsigned)((n + per - 1) / per); 
 template <typename T>
 cudaError_t quant_int8(const QuantInt8Params& p, cudaStream_t s) {
   // the fewest warps that keep a row in registers
-  if (p.K <= 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 1>>(blocks(p.rows, 8), kThreads, 0, 1, s, p);
-  else if (p.K <= 2 * 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 2>>(blocks(p.rows, 4), kThreads, 0, 1, s, p);
-  else if (p.K <= 4 * 512 * kKeep) return launch_cluster<quant_int8_kernel<T, 4>>(blocks(p.rows, 2), kThreads, 0, 1, s, p);
+  if (p.K <= 32 * kChunk * kKeep) return launch_cluster<quant_int8_kernel<T, 1>>(blocks(p.rows, 8), kThreads, 0, 1, s, p);
+  else if (p.K <= 2 * 32 * kChunk * kKeep) return launch_cluster<quant_int8_kernel<T, 2>>(blocks(p.rows, 4), kThreads, 0, 1, s, p);
+  else if (p.K <= 4 * 32 * kChunk * kKeep) return launch_cluster<quant_int8_kernel<T, 4>>(blocks(p.rows, 2), kThreads, 0, 1, s, p);
   else return launch_cluster<quant_int8_kernel<T, 8>>(p.rows, kThreads, 0, 1, s, p);
 }
 
