@@ -47,8 +47,15 @@ struct Cfg {
 // rows and their weights in the L2.
 constexpr int kBand = 8;
 
-// Contraction steps (128 bytes each) that a share of a split tile keeps.
-constexpr int kMinChunks = 4;
+// A contraction of fewer steps (128 bytes each) is not split, and a share
+// keeps kMinChunks.  Joining costs about 2 us; B200, 16 rows by 512 features:
+// 8 steps 5.0 us whole and 6.1 in two, 16 steps 7.0 in two and 6.4 in four.
+constexpr int kSplitChunks = 12, kMinChunks = 4;
+// From this many steps on, few large tiles are cut into 64 rows and their
+// contraction split instead of being given to pairs: 512 x 512 features, 16
+// steps 10.4 us so and 8.2 on pairs; 300 x 256, 32 steps 9.1 and 11.3; 256 x
+// 512, 112 steps 13.6 and 29.1.
+constexpr int kFewChunks = 24;
 
 // Units are handed out at run time from this many contraction steps on, when
 // there are several groups; a pair asks for its next unit kAhead steps before
@@ -533,24 +540,29 @@ GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
   // Rows a tile should hold: the group's when there is one, else twice the
   // average, since routed groups vary.
   const long long want = p.E == 1 ? p.P : 2LL * ((p.P + p.E - 1) / p.E);
+  const int chunks = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
+  const long long groups = p.E < p.P ? p.E : p.P;  // that can have rows
+  // most tiles there can be: one for each group with rows, one for each full tile
+  auto most = [&](int rows, int features) {
+    return (groups + p.P / rows) * (long long)((p.M + features - 1) / features);
+  };
   GroupedTile t{want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 256, 1, 1, sms, sms};
+  // Few tiles of 64 rows: shared contractions instead of pairs on a few SMs.
+  if (t.rows == 256 && most(64, 128) * 2 <= sms && chunks >= kFewChunks) t.rows = 64;
   if (t.rows == 256) {
     t.ctas = 2;
     t.grid = t.running = sms / 2 * 2;
-    const int steps = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
     // a cluster for every unit there can be: tiles, and the pieces of the last wave
-    const long long units = ((p.E < p.P ? p.E : p.P) + p.P / 256) * (long long)((p.M + 255) / 256) + sms / 2;
-    if (p.E > 1 && steps >= kHandOutChunks && units * 2 < (1LL << 30)) t.grid = (int)units * 2;
+    const long long units = most(256, 256) + sms / 2;
+    if (p.E > 1 && chunks >= kHandOutChunks && units * 2 < (1LL << 30)) t.grid = (int)units * 2;
     return t;
   }
-  // Few tiles (at most one per group with rows, and one per full tile): share
-  // the contraction while every share keeps kMinChunks steps and all CTAs
-  // are resident at once; each cluster then takes one tile.
-  const int chunks = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
-  const long long most = ((p.E < p.P ? p.E : p.P) + p.P / t.rows) * (long long)((p.M + 127) / 128);
+  // Few tiles: share the contraction while every share keeps kMinChunks steps
+  // and all CTAs are resident at once; each cluster then takes one tile.
+  const long long tiles = most(t.rows, 128);
   const int limit = t.rows <= 32 ? 8 : 4;
-  while (t.split < limit && most * t.split * 2 <= sms && chunks >= t.split * 2 * kMinChunks) t.split *= 2;
-  if (t.split > 1) t.grid = (int)most * t.split;
+  while (chunks >= kSplitChunks && t.split < limit && tiles * t.split * 2 <= sms && chunks >= t.split * 2 * kMinChunks) t.split *= 2;
+  if (t.split > 1) t.grid = (int)tiles * t.split;
   return t;
 }
 

@@ -191,6 +191,33 @@ def test_slots_outside_are_skipped():
     assert (q[[1, 3, 5]] == 5).all() and (s[[1, 3, 5]] == 5.0).all() and torch.equal(q[0], q[2])
 
 
+def test_the_same_row_twice():
+    """combine may read a row for several slots, and permute a token for several rows."""
+    y = torch.randn(3, 40, device="cuda")
+    inv = torch.tensor([2, 2, 0, 2], dtype=torch.int32, device="cuda")
+    g = torch.tensor([[0.5, 0.25], [2.0, -1.0]], device="cuda")
+    out = moe.combine(y, inv, g)
+    ref = torch.stack([0.75 * y[2].double(), 2 * y[0].double() - y[2].double()])
+    assert ((out.double() - ref).abs() <= 4 * 2.0 ** -24 * (y[2].abs() + 2 * y[0].abs()).double()).all()
+    perm = torch.tensor([5, 5, 4], dtype=torch.int32, device="cuda")
+    assert torch.equal(moe.permute(y, perm, 2), y[[2, 2, 2]])
+
+
+def test_infinite_weights_and_values_are_kept_apart():
+    """A token's NaN or infinity reaches that token's output only."""
+    T, k, H = 3, 2, 24
+    y = torch.randn(T * k, H, device="cuda")
+    y[1, 3] = float("inf")
+    y[4, 5] = float("nan")
+    inv = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    g = torch.rand(T, k, device="cuda") + 0.1
+    out = moe.combine(y, inv, g)
+    ref = (g[..., None].double() * y.view(T, k, H).double()).sum(1)
+    assert torch.equal(torch.isnan(out), torch.isnan(ref)) and torch.equal(torch.isinf(out), torch.isinf(ref))
+    fine = torch.isfinite(ref)
+    assert torch.allclose(out.double()[fine], ref[fine], rtol=1e-6, atol=1e-6)
+
+
 # ---- row quantisation -----------------------------------------------------------------
 def quant64(x):
     """Codes and scales by the definition; every quotient 127 x / amax of 16-bit values is far from a tie unless it

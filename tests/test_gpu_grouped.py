@@ -247,6 +247,94 @@ def test_unusable_offsets_compute_nothing(off):
         assert (out == 5.0).all()
 
 
+# Shapes that reach every way a call is tiled on 148 SMs: rows per tile, shares
+# of the contraction, pairs, pieces of the last wave, units handed out at run time.
+WAYS = {
+    "rows16": ([9, 3], 4000, 136),
+    "rows16_split8": ([7], 520, 4160),
+    "rows16_split4": ([3, 0, 9], 1160, 2056),
+    "rows32_split2": ([20, 5, 12, 9], 1032, 1096),
+    "rows32": ([13, 9, 20, 2, 10], 2056, 136),
+    "rows64_split4": ([60], 136, 3080),
+    "rows64_few_large": ([300, 0, 41], 264, 2056),
+    "rows64": ([31, 33, 20, 40], 1032, 328),
+    "pairs": ([300, 500, 65, 129], 2056, 520),
+    "pairs_pieces": ([2048], 1288, 648),
+    "pairs_handed_out": ([700, 3, 333, 0, 512, 1100], 2824, 2056),
+    "pairs_handed_out_few_units": ([257, 64, 130, 0, 0, 0, 1], 1544, 2120),
+}
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_every_tiling(way):
+    counts, N, K = WAYS[way]
+    off = offsets_of(counts)
+    P, E = sum(counts), len(counts)
+    gen = torch.Generator("cuda").manual_seed(N)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w, x = randn(gen, E, N, K, dtype=BF16), randn(gen, P, K, dtype=BF16)
+    y = moe.grouped_gemm(x, w, off, out_dtype=FP32, status=status)
+    ref, A = forward64(x, w, off)
+    check(y, ref, tol16(ref, A, K, FP32))
+    assert torch.equal(y, moe.grouped_gemm(x, w, off, out_dtype=FP32))   # no sum depends on timing
+    # the gradient's contraction runs over w's rows: the same tiling with the sizes exchanged
+    wt = w.transpose(1, 2).contiguous()
+    dx = moe.grouped_gemm_dgrad(x, wt, off, out_dtype=FP32, status=status)
+    check(dx, ref, tol16(ref, A, K, FP32))
+    K8 = 2 * (K // 16 * 16)   # as many steps of 128 bytes
+    q = torch.randint(-128, 128, (P, K8), generator=gen, device="cuda", dtype=torch.int8)
+    w8 = torch.randint(-128, 128, (E, N, K8), generator=gen, device="cuda", dtype=torch.int8)
+    s, c = torch.rand(P, generator=gen, device="cuda"), torch.rand(E, N, generator=gen, device="cuda")
+    for out in (BF16, FP32):
+        y = moe.int8_gemm(q, s, w8, c, offsets=off, out_dtype=out, status=status)
+        check_int8(y, int8_64(q, s, w8, c, off), out)
+    assert int(status) == 0
+
+
+def test_weight_gradient_tilings():
+    """Whole waves of tiles, halves of the last wave, and more experts than the larger pipeline has room for."""
+    gen = torch.Generator("cuda").manual_seed(12)
+    for counts, N, K in (([200, 0, 77], 1800, 3336), ([64] * 37, 264, 520), ([3, 0, 1, 20] * 130, 136, 72),
+                         ([5000], 520, 392)):
+        off = offsets_of(counts)
+        P = sum(counts)
+        dy, x = randn(gen, P, N, dtype=FP16), randn(gen, P, K, dtype=FP16)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        dw = moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32, status=status)
+        ref, A = wgrad64(dy, x, off)
+        check(dw, ref, tol16(ref, A, max(counts), FP32))
+        assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)) and int(status) == 0
+
+
+def test_more_than_2_to_31_elements():
+    """Rows that start past 2^31 elements, of the operands and of the outputs."""
+    P, K, N, n = 263000, 8200, 16, 300     # P * K = 2.16e9
+    x = torch.zeros(P, K, dtype=BF16, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(13)
+    x[-n:] = randn(gen, n, K, dtype=BF16)
+    w = randn(gen, 2, N, K, dtype=BF16)
+    off = torch.tensor([0, P - n // 2, P], dtype=torch.int32, device="cuda")
+    tail = torch.tensor([0, n // 2, n], dtype=torch.int32, device="cuda")
+    y = moe.grouped_gemm(x, w, off, out_dtype=FP32)
+    ref, A = forward64(x[-n:], w, tail)
+    check(y[-n:], ref, tol16(ref, A, K, FP32))
+    assert not y[:-n].any()
+    dw = moe.grouped_gemm_wgrad(y.to(BF16), x, off, out_dtype=FP32)
+    ref, A = wgrad64(y[-n:].to(BF16), x[-n:], tail)
+    check(dw, ref, tol16(ref, A, n, FP32))
+    moe.grouped_gemm_dgrad(y.to(BF16), w, off, out=x)
+    ref, A = forward64(y[-n:].to(BF16), w, tail, "n")
+    check(x[-n:], ref, tol16(ref, A, N, BF16))
+    q, s = moe.quant_int8(x)
+    q2, s2 = moe.quant_int8(x[-n:].contiguous())
+    assert torch.equal(q[-n:], q2) and torch.equal(s[-n:], s2)
+    perm = torch.arange(P, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    moved = moe.permute(x, perm, 1)
+    assert torch.equal(moved[:n], x[-n:].flip(0))
+    back = moe.combine(moved, perm, k=1)
+    assert torch.equal(back[-n:], x[-n:])
+
+
 def test_no_rows():
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
     w = torch.ones(3, 16, 64, dtype=BF16, device="cuda")
@@ -346,6 +434,39 @@ def test_two_streams_at_once():
         for a, b in zip(alone, both):
             for u, v in zip(a, b):
                 assert torch.equal(u, v)
+
+
+def test_two_graphs_replayed_at_once():
+    """Two captured graphs of the same calls run side by side: there is no shared workspace."""
+    gen = torch.Generator("cuda").manual_seed(17)
+    counts = [40, 0, 7, 300, 21]
+    off, P, E, N, K = offsets_of(counts), sum(counts), len(counts), 520, 2056
+    sets, graphs = [], []
+    for i in range(2):
+        x, w, dy = randn(gen, P, K, dtype=BF16), randn(gen, E, N, K, dtype=BF16), randn(gen, P, N, dtype=BF16)
+        w8 = torch.randint(-128, 128, (E, N, K + 8), generator=gen, device="cuda", dtype=torch.int8)[:, :, :K]
+
+        def step(x=x, w=w, dy=dy, w8=w8):
+            q, s = moe.quant_int8(x)   # (rows of K = 2056 bytes, padded to a multiple of 16)
+            return (moe.grouped_gemm(x, w, off), moe.grouped_gemm_dgrad(dy, w, off), moe.grouped_gemm_wgrad(dy, x, off),
+                    moe.int8_gemm(q, s, w8, torch.ones(E, N, device="cuda"), offsets=off))
+        alone = step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        sets.append((alone, out, torch.cuda.Stream(), step))   # (step keeps the graph's inputs alive)
+        graphs.append(g)
+    for _ in range(5):
+        for g, (_, out, st, _) in zip(graphs, sets):
+            with torch.cuda.stream(st):
+                for t in out:
+                    t.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        for alone, out, _, _ in sets:
+            for a, b in zip(alone, out):
+                assert torch.equal(a, b)
 
 
 # ---- int8 ----------------------------------------------------------------------
