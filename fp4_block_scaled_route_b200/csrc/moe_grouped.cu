@@ -561,7 +561,9 @@ GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
   // and all CTAs are resident at once; each cluster then takes one tile.
   const long long tiles = most(t.rows, 128);
   const int limit = t.rows <= 32 ? 8 : 4;
-  while (chunks >= kSplitChunks && t.split < limit && tiles * t.split * 2 <= sms && chunks >= t.split * 2 * kMinChunks) t.split *= 2;
+  while (chunks >= kSplitChunks && t.split < limit && tiles <= resident_clusters(t.split * 2, sms) &&
+         chunks >= t.split * 2 * kMinChunks)
+    t.split *= 2;
   if (t.split > 1) t.grid = (int)tiles * t.split;
   return t;
 }

@@ -200,9 +200,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
 // Arrive on a barrier (in both CTAs of a pair, at the same place) once the
 // MMAs that this warp's elected lane issued so far completed.  Called by a
 // whole warp.  One commit for both CTAs: a commit each costs the issuing warp
-// another 60 cycles per step.
+// another 60 cycles per step.  `both` names the pair's CTAs in their cluster.
 template <int CG>
-__device__ __forceinline__ void mma_commit_all(uint32_t bar) {
+__device__ __forceinline__ void mma_commit_all(uint32_t bar, uint16_t both = 3) {
   if constexpr (CG == 1)
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
@@ -213,7 +213,7 @@ __device__ __forceinline__ void mma_commit_all(uint32_t bar) {
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
             bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(both)
         : "memory");
 }
 template <int CG>

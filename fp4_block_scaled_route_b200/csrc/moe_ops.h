@@ -40,6 +40,7 @@ struct WgradParams {
   int out_type, fmt;
   int32_t* status;
   uint32_t idesc;
+  int split;                // pairs that share a tile's rows
 };
 
 // Token of a routing slot: t * k + j for routed slots, T * k + t for the
@@ -106,6 +107,13 @@ cudaError_t launch_quant_int8(const QuantInt8Params& p, int dtype, cudaStream_t 
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);
 cudaError_t launch_row_combine(const RowCombineParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_row_combine_bwd(const RowCombineBwdParams& p, int dtype, cudaStream_t s);
+
+// Clusters of `size` CTAs, one CTA per SM, that are resident at once: the SMs
+// of a GPC do not all fit clusters of 4 and 8 (B200, 148 SMs, as the occupancy
+// query gives it: 74 of 2, 33 of 4, 15 of 8).
+inline int resident_clusters(int size, int sms) {
+  return size <= 2 ? sms / size : size <= 4 ? sms * 33 / 148 : sms * 15 / 148;
+}
 
 // Launch as a programmatic dependent of the kernel before it in the stream
 // (the kernels wait, before they read anything, until that one is complete),

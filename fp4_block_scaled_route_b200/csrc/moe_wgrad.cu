@@ -1,5 +1,7 @@
 // moe_wgrad.cu -- weight gradients of the ragged grouped product:
 // dW_e[n, k] = sum over the rows p of group e of dy[p, n] x[p, k].
+#include <type_traits>
+
 #include "moe_grouped.cuh"
 
 namespace moe {
@@ -30,7 +32,7 @@ struct WCfg {
   static constexpr int BARS = 512;
   static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * OUT + BARS;  // (+ the offsets)
   static constexpr int MAX_E = (232448 - SMEM) / 4 - 1;
-  static_assert((4 * STAGES + 5) * 8 + 8 <= BARS && MAX_E > 0, "shared memory");
+  static_assert((4 * STAGES + 7) * 8 + 8 <= BARS && MAX_E > 0, "shared memory");
 };
 
 // Work of one pair: all features of an expert before the next column of
@@ -92,7 +94,10 @@ struct WWalk {
   }
 };
 
-template <int STAGES>
+// SPLIT: p.split pairs of a cluster share a tile's rows; each then sends the
+// others their part of the columns of its sums, adds up its own part in the
+// pairs' order, and stores it.
+template <int STAGES, bool SPLIT>
 __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                  const __grid_constant__ CUtensorMap tmO, const WgradParams p) {
@@ -106,14 +111,20 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   uint64_t* zeroed = part + STAGES;     // (even CTA) both CTAs have zeroed the tail
   uint64_t* tfull = zeroed + STAGES;    // a commit to each CTA
   uint64_t* tempty = tfull + 2;         // (even CTA) the epilogue warps of both CTAs
-  uint64_t* done = tempty + 2;
+  uint64_t* ready = tempty + 2;         // (SPLIT) the other pairs' memory is free
+  uint64_t* joined = ready + 1;         // (SPLIT) their sums are here
+  uint64_t* done = joined + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + C::BARS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
-  const int team = blockIdx.x / 2, teams = gridDim.x / 2;
+  // rank: of the CTA in its pair; pair: of the pair in its cluster
+  const int split = SPLIT ? p.split : 1;
+  const int rank = (int)cluster_rank() & 1, pair = SPLIT ? (int)cluster_rank() >> 1 : 0;
+  const uint32_t even = 2 * pair;                       // the pair's even CTA in the cluster
+  const uint16_t both = (uint16_t)(3u << (2 * pair));   // its two CTAs
+  const int team = blockIdx.x / (2 * split), teams = gridDim.x / (2 * split);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -124,6 +135,10 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * C::EPI_WARPS);
+    }
+    if (SPLIT) {
+      mbar_init(ready, (split - 1) * C::EPI_WARPS);
+      mbar_init(joined, (split - 1) * C::EPI_WARPS);
     }
     mbar_init(done, 1);
     *abort = 0;
@@ -152,16 +167,26 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   const uint32_t tmem = *tmem_holder;
   // (a unit's place in the walk: the same for every role)
   WWalk walk(s_off, bad ? 0 : p.E, p.N, p.K, team, teams);
+  // The next unit, with this pair's share of the rows: whole stages of them.
+  auto take = [&](WUnit& t) {
+    if (!walk.take(t, teams)) return false;
+    if (SPLIT) {
+      const int lo = t.lo, stages = (t.hi - lo + C::CH - 1) / C::CH;
+      t.lo = min(t.hi, lo + (int)((long long)stages * pair / split) * C::CH);
+      t.hi = min(t.hi, lo + (int)((long long)stages * (pair + 1) / split) * C::CH);
+    }
+    return true;
+  };
   // A stage's last rows are zeroed when they end inside a 16-row MMA step.
   auto ragged = [](int held) { return held < C::CH && (held & 15); };
 
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
-    const uint32_t full0 = mapa_rank(full, 0), part0 = mapa_rank(part, rank);
+    const uint32_t full0 = mapa_rank(full, even), part0 = mapa_rank(part, even + rank);
     uint32_t armed = 0, armed_part = 0, uses = 0, st = 0, ph = 0;
     bool ok = true;
     WUnit t;
-    while (ok && walk.take(t, teams)) {
+    while (ok && take(t)) {
       if (t.k0 >= p.K) continue;
       const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 64 * t.nb, nb = t.nb;
       const uint32_t bytes = (2 + nb) * C::BOX;
@@ -211,12 +236,12 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     bool ok = true;
     int j = 0;
     WUnit next;
-    bool more = walk.take(next, teams);
+    bool more = take(next);
     while (more && ok) {
       const WUnit t = next;
       const int lo = t.lo, hi = t.hi, nb = t.nb;
       if (hi == lo || t.k0 >= p.K) {
-        more = walk.take(next, teams);
+        more = take(next);
         continue;
       }
       const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
@@ -244,18 +269,18 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
           for (int kk = 0; kk < steps; ++kk)
             mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != lo) | (kk != 0));
         }
-        mma_commit_all<2>(empty0 + 8u * st);
+        mma_commit_all<2>(empty0 + 8u * st, both);
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
         }
         // the next unit is looked up while the tensor cores have work
-        if (row == lo) more = walk.take(next, teams);
+        if (row == lo) more = take(next);
       }
-      if (ok) mma_commit_all<2>(tfull0 + 8u * buf);
+      if (ok) mma_commit_all<2>(tfull0 + 8u * buf, both);
       ++j;
     }
-    mma_commit_all<2>(smem_u32(done));
+    mma_commit_all<2>(smem_u32(done), both);
     mbar_drain(done, 0);
     __syncwarp();
   } else if (warp == 2) {
@@ -265,11 +290,11 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     // box, whatever the swizzle does inside it.  Each CTA's warp 2 does so in
     // its own shared memory, ahead of the warp that issues the MMAs: done by
     // that warp it cost 15 % of the time at 512 rows a group.
-    const uint32_t zeroed0 = mapa_rank(zeroed, 0);
+    const uint32_t zeroed0 = mapa_rank(zeroed, even);
     uint32_t uses = 0, st = 0;
     bool ok = true;
     WUnit t;
-    while (ok && walk.take(t, teams)) {
+    while (ok && take(t)) {
       if (t.hi == t.lo || t.k0 >= p.K) continue;
       const int rows = t.hi - t.lo, last = (rows - 1) / C::CH;
       if (ragged(rows - last * C::CH)) {
@@ -295,7 +320,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     // Two warps per quarter of the rows, one for each half of the columns; a
     // step is a box of 32 rows by 128 bytes.
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tempty0 = mapa_rank(tempty, 0);
+    const uint32_t tempty0 = mapa_rank(tempty, even);
     uint8_t* box = out + (warp - 4) * C::OUT;
     uint8_t* line = box + lane * 128;  // 16-byte piece i of a line sits at i ^ (lane & 7)
     const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
@@ -304,7 +329,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     bool ok = true;
     int j = 0;
     WUnit t;
-    while (ok && walk.take(t, teams)) {
+    while (ok && take(t)) {
       if (t.k0 >= p.K) continue;
       const int n = t.n0 + rank * 128 + q * 32, wide = 64 * t.nb, k0 = t.k0 + half * wide;
       const bool none = t.hi == t.lo;
@@ -314,6 +339,84 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
+      }
+      if (SPLIT) {
+        // Every pair owns 1 / split of the tile's columns, of which this warp
+        // takes half, in blocks of 16.  A pair's sums go straight into the
+        // owners' pipeline memory, which is free once their MMAs are done:
+        // [sender][warp][block][register / 4][lane][4] words.
+        const int part = 128 * t.nb / split, blocks = part / 32;
+        uint32_t* sums = reinterpret_cast<uint32_t*>(smem);
+        const uint32_t row_acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * (part / 2);
+        auto sums_at = [&](int sender, int b) {
+          return sums + (((sender * C::EPI_WARPS + (warp - 4)) * blocks + b) * 16 * 32) + lane * 4;
+        };
+        auto own = [&](int pr, int b, float (&v)[16]) {
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+          } else {
+            tmem_ld16(row_acc + pr * part + b * 16, v);
+            tmem_wait_ld();
+          }
+        };
+        __syncwarp();
+        for (int pr = 0; pr < split; ++pr)
+          if (pr != pair && lane == 0) mbar_arrive_at(mapa_rank(ready, 2 * pr + rank));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(ready, 0, abort));
+        if (!ok) break;
+        for (int pr = 0; pr < split; ++pr) {
+          if (pr == pair) continue;
+          for (int b = 0; b < blocks; ++b) {
+            float v[16];
+            own(pr, b, v);
+            const uint32_t to = mapa_rank(sums_at(pair, b), 2 * pr + rank);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              st_cluster_v4(to + i * 512, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(mapa_rank(joined, 2 * pr + rank));
+        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(joined, 0, abort));
+        if (!ok) break;
+        for (int b = 0; b < blocks; ++b) {
+          float mine[16], v[16];
+          own(pair, b, mine);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+          for (int pr = 0; pr < split; ++pr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float4 o = make_float4(mine[4 * i], mine[4 * i + 1], mine[4 * i + 2], mine[4 * i + 3]);
+              if (pr != pair) o = *reinterpret_cast<const float4*>(sums_at(pr, b) + i * 128);
+              v[4 * i] += o.x;
+              v[4 * i + 1] += o.y;
+              v[4 * i + 2] += o.z;
+              v[4 * i + 3] += o.w;
+            }
+          }
+          const int k = t.k0 + pair * part + half * (part / 2) + b * 16;
+          const size_t at = ((size_t)t.e * p.N + n + lane) * p.K + k;
+          // (K is a multiple of 16 bytes: no piece is partly inside)
+          if (n + lane >= p.N) continue;
+          if (f32) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              if (k + i < p.K)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at + i) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              if (k + i < p.K)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw) + at + i) =
+                    make_uint4(pack16(v[i], v[i + 1], bf), pack16(v[i + 2], v[i + 3], bf),
+                               pack16(v[i + 4], v[i + 5], bf), pack16(v[i + 6], v[i + 7], bf));
+          }
+        }
+        break;  // a cluster has one tile
       }
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * wide;
       for (int c = 0; c < wide && k0 + c < p.K && n < p.N; c += width) {
@@ -367,11 +470,25 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
                          int sms, cudaStream_t s) {
   WgradParams p = p0;
   p.idesc = idesc_f16(kWM, 0, p.fmt, 1, 1);  // N is set tile by tile
-  const size_t table = (p.E + 1) * sizeof(int32_t);
+  // Few tiles of many rows: 2 or 4 pairs share a tile while each has kMinStages
+  // stages and all are resident.  B200, 4096 rows into 512 x 512: 22.0 us
+  // whole, 17.7 in two, 15.6 in four; 16384 into 1024 x 1024: 76 whole, 46 in
+  // two; 1000 into 384 x 176 (16 stages): 8.9 whole, 11.0 in two.
+  constexpr int kMinStages = 16;
+  const long long tiles = (long long)p.E * ((p.N + kWM - 1) / kWM) * ((p.K + kWN - 1) / kWN);
+  const int stages = (int)((p.P / p.E + 63) / 64);
+  p.split = 1;
+  while (p.split < 4 && tiles <= resident_clusters(p.split * 4, sms) && stages >= p.split * 2 * kMinStages)
+    p.split *= 2;
+  const int grid = p.split > 1 ? (int)tiles * p.split * 2 : sms / 2 * 2;
+  auto go = [&](auto n) {
+    using C = WCfg<n>;
+    const size_t smem = C::SMEM + (p.E + 1) * sizeof(int32_t);
+    return p.split > 1 ? launch_cluster<wgrad_kernel<n, true>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, p)
+                       : launch_cluster<wgrad_kernel<n, false>>(grid, C::THREADS, smem, 2, s, ty, tx, to, p);
+  };
   static_assert(WCfg<5>::MAX_E >= 1024, "every expert count has a variant");
-  if (p.E <= WCfg<6>::MAX_E)
-    return launch_cluster<wgrad_kernel<6>>(sms / 2 * 2, WCfg<6>::THREADS, WCfg<6>::SMEM + table, 2, s, ty, tx, to, p);
-  return launch_cluster<wgrad_kernel<5>>(sms / 2 * 2, WCfg<5>::THREADS, WCfg<5>::SMEM + table, 2, s, ty, tx, to, p);
+  return p.E <= WCfg<6>::MAX_E ? go(std::integral_constant<int, 6>{}) : go(std::integral_constant<int, 5>{});
 }
 
 }  // namespace moe

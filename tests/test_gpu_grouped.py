@@ -252,6 +252,8 @@ def test_unusable_offsets_compute_nothing(off):
 WAYS = {
     "rows16": ([9, 3], 4000, 136),
     "rows16_split8": ([7], 520, 4160),
+    "rows16_split8_at_most": ([16], 1912, 4104),
+    "rows16_split2": ([3, 2, 9], 2056, 1032),
     "rows16_split4": ([3, 0, 9], 1160, 2056),
     "rows32_split2": ([20, 5, 12, 9], 1032, 1096),
     "rows32": ([13, 9, 20, 2, 10], 2056, 136),
@@ -292,10 +294,12 @@ def test_every_tiling(way):
 
 
 def test_weight_gradient_tilings():
-    """Whole waves of tiles, halves of the last wave, and more experts than the larger pipeline has room for."""
+    """Whole waves of tiles, halves of the last wave, more experts than the larger pipeline has room for, and few tiles
+    whose rows two or four pairs share (some of them without any)."""
     gen = torch.Generator("cuda").manual_seed(12)
     for counts, N, K in (([200, 0, 77], 1800, 3336), ([64] * 37, 264, 520), ([3, 0, 1, 20] * 130, 136, 72),
-                         ([5000], 520, 392)):
+                         ([5000], 520, 392), ([2100], 136, 200), ([1, 0, 4000, 63], 264, 136), ([1300, 1000], 504, 776),
+                         ([3001], 40, 8)):
         off = offsets_of(counts)
         P = sum(counts)
         dy, x = randn(gen, P, N, dtype=FP16), randn(gen, P, K, dtype=FP16)
@@ -304,6 +308,8 @@ def test_weight_gradient_tilings():
         ref, A = wgrad64(dy, x, off)
         check(dw, ref, tol16(ref, A, max(counts), FP32))
         assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)) and int(status) == 0
+        dw = moe.grouped_gemm_wgrad(dy, x, off)
+        check(dw, ref, tol16(ref, A, max(counts), FP16))
 
 
 def test_more_than_2_to_31_elements():
