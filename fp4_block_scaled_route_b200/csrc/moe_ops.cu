@@ -176,12 +176,16 @@ moe_status moe_grouped_gemm_wgrad(int dtype, int out_dtype, int E, int P, int N,
   p.dw = dw; p.out_type = out_dtype;
   p.fmt = dtype == MOE_DT_BF16 ? 1 : 0;
   p.status = d_status;
-  CUtensorMap ty, tx, to;
+  p.dy = static_cast<const uint16_t*>(dy); p.lddy = lddy;
+  p.x = static_cast<const uint16_t*>(x); p.ldx = ldx;
+  CUtensorMap ty, tx, to, ty16, tx16;
   if (!make_map(&ty, map_type(dtype), 2, dy, N, P, lddy, 0, 0, 64) ||
       !make_map(&tx, map_type(dtype), 2, x, K, P, ldx, 0, 0, 64) ||
+      !make_map(&ty16, map_type(dtype), 2, dy, N, P, lddy, 0, 0, 16) ||
+      !make_map(&tx16, map_type(dtype), 2, x, K, P, ldx, 0, 0, 16) ||
       !make_map(&to, map_type(out_dtype), oes, dw, K, N, K, E, (long long)N * K, 32))
     return MOE_ERR_CUDA;
-  return moe::launch_wgrad(ty, tx, to, p, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return moe::launch_wgrad(ty, tx, to, ty16, tx16, p, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_int8_gemm(int out_dtype, int E, int P, int N, int K, const int32_t* offsets, const int8_t* q,

@@ -36,6 +36,9 @@ struct GroupedParams {
 struct WgradParams {
   int E, P, N, K;
   const int32_t* offsets;
+  const uint16_t* dy;       // [P, N], row stride lddy
+  const uint16_t* x;        // [P, K], row stride ldx
+  long long lddy, ldx;
   void* dw;                 // [E, N, K]
   int out_type, fmt;
   int32_t* status;
@@ -100,9 +103,9 @@ struct GroupedTile {
 GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms);
 cudaError_t launch_grouped(int kind, GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx,
                            const CUtensorMap& txs, const GroupedParams& p, cudaStream_t s);
-// ty, tx: boxes of 64 rows; to: dw [E][N][K] with boxes of 32 rows.
-cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to, const WgradParams& p,
-                         int sms, cudaStream_t s);
+// ty, tx: boxes of 64 rows; ty16, tx16: of 16; to: dw [E][N][K] with boxes of 32.
+cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to, const CUtensorMap& ty16,
+                         const CUtensorMap& tx16, const WgradParams& p, int sms, cudaStream_t s);
 cudaError_t launch_quant_int8(const QuantInt8Params& p, int dtype, cudaStream_t s);
 cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);
 cudaError_t launch_row_combine(const RowCombineParams& p, int dtype, cudaStream_t s);

@@ -14,9 +14,9 @@ namespace {
 // rows of 128 dy columns and of 128 x columns, in boxes of 64 columns whose
 // rows are 128-byte lines.
 //
-// Warp 0 loads, warp 1 (of the even CTA) issues the MMAs, warp 2 zeroes what a
-// group's last stage holds past its rows, warps 4-11 read the accumulators,
-// round them and store them by TMA from shared memory.
+// Warp 0 loads, warp 1 (of the even CTA) issues the MMAs, warp 2 fills in the
+// rows of a group that do not make up a whole MMA step, warps 4-11 read the
+// accumulators, round them and store them by TMA from shared memory.
 // Stages: 6, or 5 when the offsets of very many experts take the room.
 template <int STAGES_>
 struct WCfg {
@@ -100,16 +100,17 @@ struct WWalk {
 template <int STAGES, bool SPLIT>
 __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
-                 const __grid_constant__ CUtensorMap tmO, const WgradParams p) {
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmY16,
+                 const __grid_constant__ CUtensorMap tmX16, const WgradParams p) {
   using C = WCfg<STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out = smem + STAGES * C::STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(out + C::EPI_WARPS * C::OUT);  // (even CTA) both CTAs' bytes
   uint64_t* empty = full + STAGES;      // a commit to each CTA
-  uint64_t* part = empty + STAGES;      // this CTA's bytes of a stage whose tail has to be zeroed
-  uint64_t* zeroed = part + STAGES;     // (even CTA) both CTAs have zeroed the tail
-  uint64_t* tfull = zeroed + STAGES;    // a commit to each CTA
+  uint64_t* filled = empty + STAGES;    // (even CTA) both CTAs' warps 2 have filled in a stage's last rows
+  uint64_t* fill = filled + STAGES;     // this CTA's warp 2 may fill in a stage's last rows
+  uint64_t* tfull = fill + STAGES;      // a commit to each CTA
   uint64_t* tempty = tfull + 2;         // (even CTA) the epilogue warps of both CTAs
   uint64_t* ready = tempty + 2;         // (SPLIT) the other pairs' memory is free
   uint64_t* joined = ready + 1;         // (SPLIT) their sums are here
@@ -129,8 +130,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&part[s], 1);
-      mbar_init(&zeroed[s], 2);
+      mbar_init(&filled[s], 2);
+      mbar_init(&fill[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -146,6 +147,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     tma_prefetch_map(&tmY);
     tma_prefetch_map(&tmX);
     tma_prefetch_map(&tmO);
+    tma_prefetch_map(&tmY16);
+    tma_prefetch_map(&tmX16);
   }
   if (warp == 1) tmem_alloc_cg<2>(tmem_holder, C::TMEM_COLS);
   // everything above ran while the kernel before this one could still be
@@ -177,13 +180,16 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     }
     return true;
   };
-  // A stage's last rows are zeroed when they end inside a 16-row MMA step.
+  // Rows of a stage that TMA must not load as part of a 64-row box, because
+  // those past the group's end, in the same 16-row MMA step, may hold anything
+  // (NaN too) and have to be zero in both operands: such a stage's whole steps
+  // come by TMA in boxes of 16 rows, the rest by warp 2.
   auto ragged = [](int held) { return held < C::CH && (held & 15); };
 
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
-    const uint32_t full0 = mapa_rank(full, even), part0 = mapa_rank(part, even + rank);
-    uint32_t armed = 0, armed_part = 0, uses = 0, st = 0, ph = 0;
+    const uint32_t full0 = mapa_rank(full, even);
+    uint32_t armed = 0, st = 0, ph = 0;
     bool ok = true;
     WUnit t;
     while (ok && take(t)) {
@@ -193,26 +199,32 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
       for (int row = t.lo; row < t.hi; row += C::CH) {
         ok = mbar_wait_warp(&empty[st], ph ^ 1u, abort);
         if (!ok) break;
-        const bool rag = ragged(t.hi - row);
-        const uint32_t bar = (rag ? part0 : full0) + 8u * st;
+        const uint32_t bar = full0 + 8u * st;
         uint8_t* a = smem + st * C::STAGE;
+        const int held = t.hi - row, steps = ragged(held) ? held / 16 : 4;  // those that TMA loads
         if (elect_one()) {
-          if (rag) {
-            if (rank == 0) mbar_arrive(&full[st]);  // (no bytes: this phase only counts along)
-            mbar_arrive_expect_tx(&part[st], bytes);
+          if (steps == 0) {
+            if (rank == 0) mbar_arrive(&full[st]);
           } else if (rank == 0) {
-            mbar_arrive_expect_tx(&full[st], 2 * bytes);
+            mbar_arrive_expect_tx(&full[st], 2 * (bytes / 4) * steps);
           }
-          tma_load_2d_pair(&tmY, bar, a, n0, row, pol);
-          tma_load_2d_pair(&tmY, bar, a + C::BOX, n0 + 64, row, pol);
-          tma_load_2d_pair(&tmX, bar, a + 2 * C::BOX, k0, row, pol);
-          if (nb == 2) tma_load_2d_pair(&tmX, bar, a + 3 * C::BOX, k0 + 64, row, pol);
+          if (!ragged(held)) {
+            tma_load_2d_pair(&tmY, bar, a, n0, row, pol);
+            tma_load_2d_pair(&tmY, bar, a + C::BOX, n0 + 64, row, pol);
+            tma_load_2d_pair(&tmX, bar, a + 2 * C::BOX, k0, row, pol);
+            if (nb == 2) tma_load_2d_pair(&tmX, bar, a + 3 * C::BOX, k0 + 64, row, pol);
+          } else {
+            mbar_arrive(&fill[st]);
+            for (int g = 0; g < steps; ++g) {
+              uint8_t* ag = a + g * (C::BOX / 4);
+              tma_load_2d_pair(&tmY16, bar, ag, n0, row + 16 * g, pol);
+              tma_load_2d_pair(&tmY16, bar, ag + C::BOX, n0 + 64, row + 16 * g, pol);
+              tma_load_2d_pair(&tmX16, bar, ag + 2 * C::BOX, k0, row + 16 * g, pol);
+              if (nb == 2) tma_load_2d_pair(&tmX16, bar, ag + 3 * C::BOX, k0 + 64, row + 16 * g, pol);
+            }
+          }
         }
         armed |= 1u << st;
-        if (rag) {
-          armed_part |= 1u << st;
-          uses ^= 1u << st;
-        }
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
@@ -221,17 +233,15 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     }
     // after an abort: the copies in flight land before the CTAs leave.
     // Stages below st were last armed with parity ph, the others before.
-    if (*abort)
-      for (uint32_t s = 0; s < STAGES; ++s) {
-        if (rank == 0 && armed & (1u << s)) mbar_drain(&full[s], s < st ? ph : ph ^ 1u);
-        if (armed_part & (1u << s)) mbar_drain(&part[s], ((uses >> s) & 1u) ^ 1u);
-      }
+    if (*abort && rank == 0)
+      for (uint32_t s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) mbar_drain(&full[s], s < st ? ph : ph ^ 1u);
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     const uint32_t empty0 = smem_u32(empty), tfull0 = smem_u32(tfull);
     const uint64_t ad0 = sdesc_mn_sw128(smem_u32(smem), C::BOX);
     const uint64_t bd0 = sdesc_mn_sw128(smem_u32(smem) + 2 * C::BOX, C::BOX);
-    uint32_t uses = 0;  // parity of each stage's next use of zeroed
+    uint32_t uses = 0;  // parity of each stage's next use of filled
     uint32_t st = 0, ph = 0;
     bool ok = true;
     int j = 0;
@@ -251,11 +261,9 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
       tc_fence_after();
       for (int row = lo; row < hi; row += C::CH) {
         const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
-        // (a stage with a ragged tail: its bytes are counted elsewhere, and
-        // warp 2 of both CTAs says when they are in and the tail is zeroed)
         ok = mbar_wait_warp(&full[st], ph, abort);
         if (ok && ragged(hi - row)) {
-          ok = mbar_wait_cluster(&zeroed[st], (uses >> st) & 1u, abort);
+          ok = mbar_wait_cluster(&filled[st], (uses >> st) & 1u, abort);
           ok = __all_sync(0xFFFFFFFFu, ok);
           uses ^= 1u << st;
         }
@@ -284,36 +292,57 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     mbar_drain(done, 0);
     __syncwarp();
   } else if (warp == 2) {
-    // The rows of a stage past the group's end belong to the next group (or
-    // to no one) and may hold anything, NaN too: zeros in both operands, up
-    // to the end of the last 16-row step.  A row is one 128-byte line of each
-    // box, whatever the swizzle does inside it.  Each CTA's warp 2 does so in
-    // its own shared memory, ahead of the warp that issues the MMAs: done by
-    // that warp it cost 15 % of the time at 512 rows a group.
-    const uint32_t zeroed0 = mapa_rank(zeroed, even);
-    uint32_t uses = 0, st = 0;
+    // The last rows of a group, when they do not fill a 16-row step, and zeros
+    // behind them.  They are read into registers long before their stage is
+    // free and written as soon as it is, so that they are there before the
+    // stage's other rows.  (Zeroing the tail of a box that TMA loaded, after it
+    // had landed, cost 10 % of the time at 512 rows a group.)
+    const uint32_t filled0 = mapa_rank(filled, even);
+    uint32_t st = 0, uses = 0;  // first stage of the unit; parity of each stage's next use of fill
     bool ok = true;
     WUnit t;
     while (ok && take(t)) {
-      if (t.hi == t.lo || t.k0 >= p.K) continue;
-      const int rows = t.hi - t.lo, last = (rows - 1) / C::CH;
-      if (ragged(rows - last * C::CH)) {
-        const int held = rows - last * C::CH, pieces = ((held + 15) / 16 * 16 - held) * 8;
-        const uint32_t s = (st + last) % STAGES;
-        uint8_t* a = smem + s * C::STAGE;
-        ok = mbar_wait_warp(&part[s], (uses >> s) & 1u, abort);
-        if (!ok) break;
-        uses ^= 1u << s;
-        for (int i = lane; i < pieces; i += 32) {
-          uint4* at = reinterpret_cast<uint4*>(a + held * 128 + i * 16);
+      if (t.hi <= t.lo || t.k0 >= p.K) continue;
+      const int rows = t.hi - t.lo, stages = (rows + C::CH - 1) / C::CH, held = rows - (stages - 1) * C::CH;
+      const uint32_t s = (st + stages - 1) % STAGES;  // the last stage
+      st = (st + stages) % STAGES;
+      if (!ragged(held)) continue;
+      const int first = held & ~15, count = held & 15, row0 = t.hi - count;
+      const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 64 * t.nb;
+      // piece j of this lane: 16 bytes of one row of one box
+      uint4 v[16];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) at[b * (C::BOX / 16)] = make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 16; ++j) {
+        const int i = j * 32 + lane, box = i >> 7, r = (i >> 3) & 15, c = (box & 1) * 64 + (i & 7) * 8;
+        const int col = (box < 2 ? n0 : k0) + c, cols = box < 2 ? p.N : p.K;
+        const uint16_t* src = box < 2 ? p.dy + (long long)(row0 + r) * p.lddy + col
+                                      : p.x + (long long)(row0 + r) * p.ldx + col;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (r < count) {
+          if (col + 8 <= cols) {
+            v[j] = __ldg(reinterpret_cast<const uint4*>(src));
+          } else if (col < cols) {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (col + k < cols) w[k / 2] |= (uint32_t)src[k] << (16 * (k & 1));
+            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(zeroed0 + 8u * s);
       }
-      st = (st + last + 1) % STAGES;
+      ok = mbar_wait_warp(&fill[s], (uses >> s) & 1u, abort);
+      if (!ok) break;
+      uses ^= 1u << s;
+      uint8_t* a = smem + s * C::STAGE + first * 128;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int i = j * 32 + lane, box = i >> 7, r = (i >> 3) & 15;
+        // (`first` is a multiple of 16 lines: the swizzle goes by r alone)
+        *reinterpret_cast<uint4*>(a + box * C::BOX + r * 128 + (((i & 7) ^ (r & 7)) * 16)) = v[j];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(filled0 + 8u * s);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -466,8 +495,9 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to, const WgradParams& p0,
-                         int sms, cudaStream_t s) {
+cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to,
+                         const CUtensorMap& ty16, const CUtensorMap& tx16, const WgradParams& p0, int sms,
+                         cudaStream_t s) {
   WgradParams p = p0;
   p.idesc = idesc_f16(kWM, 0, p.fmt, 1, 1);  // N is set tile by tile
   // Few tiles of many rows: 2 or 4 pairs share a tile while each has kMinStages
@@ -484,8 +514,8 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
   auto go = [&](auto n) {
     using C = WCfg<n>;
     const size_t smem = C::SMEM + (p.E + 1) * sizeof(int32_t);
-    return p.split > 1 ? launch_cluster<wgrad_kernel<n, true>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, p)
-                       : launch_cluster<wgrad_kernel<n, false>>(grid, C::THREADS, smem, 2, s, ty, tx, to, p);
+    return p.split > 1 ? launch_cluster<wgrad_kernel<n, true>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, ty16, tx16, p)
+                       : launch_cluster<wgrad_kernel<n, false>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
   };
   static_assert(WCfg<5>::MAX_E >= 1024, "every expert count has a variant");
   return p.E <= WCfg<6>::MAX_E ? go(std::integral_constant<int, 6>{}) : go(std::integral_constant<int, 5>{});

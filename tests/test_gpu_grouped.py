@@ -299,7 +299,7 @@ def test_weight_gradient_tilings():
     gen = torch.Generator("cuda").manual_seed(12)
     for counts, N, K in (([200, 0, 77], 1800, 3336), ([64] * 37, 264, 520), ([3, 0, 1, 20] * 130, 136, 72),
                          ([5000], 520, 392), ([2100], 136, 200), ([1, 0, 4000, 63], 264, 136), ([1300, 1000], 504, 776),
-                         ([3001], 40, 8)):
+                         ([3001], 40, 8), ([1, 4099, 70, 2111] * 5, 520, 1032)):
         off = offsets_of(counts)
         P = sum(counts)
         dy, x = randn(gen, P, N, dtype=FP16), randn(gen, P, K, dtype=FP16)
