@@ -2,6 +2,25 @@
 // side: y[p, :] = x[p, :] W_e^T (forward), dx[p, :] = dy[p, :] W_e (input
 // gradient), and the 8-bit integer product y[p, n] = s[p] c[e, n]
 // sum_k q[p, k] w[e, n, k], for the rows p of every group e.
+//
+// Weights are the M operand and rows the N operand because a group has any
+// number of rows: an MMA's N goes down to 16 (32 for a pair), so a group of a
+// few rows costs little more than streaming its weights, and one kernel serves
+// both a decode step and a prefill.  The contraction index of the rows is
+// contiguous; that of the weights is too in the forward product (K-major
+// tiles), and is their row index in the input gradient (MN-major tiles, no
+// transposed copy).  Rows of other groups inside a tile are loaded, multiplied
+// and not stored: they reach no other row's sums.
+//
+// What bounds it.  Few rows per group: the weights' stream from HBM (256
+// experts, 256 rows, 7168 x 2048 bf16: 698 us, 6.9 TB/s).  Many: the tensor
+// cores at the power limit.  Tiles are 256 x 256 on CTA pairs, because a pair
+// moves 64 KB into shared memory per step where two CTAs alone move 96, and
+// the L2 delivers little more than that: with a quarter of the loads left out
+// the dense product took 320 us instead of 352.  32 ragged groups of 32768
+// rows, 4096 x 7168: 1643 us, 1.17 PFLOP/s, about 1.1 GHz at 1000 W (the
+// library's dense product of the same size sustains 1.40); dense 8192 rows:
+// 325 us, 1.48 PFLOP/s (310 us).  8-bit: 8192 x 4096 x 7168 159 us, 3.0 POP/s.
 #include "moe_grouped.cuh"
 
 namespace moe {
@@ -10,9 +29,14 @@ namespace {
 // Tiles of 128 * CG output features by BN rows.  CG = 1: one CTA; CG = 2: a
 // pair of CTAs, each with half of the features and half of the rows' operand
 // in its shared memory.  SPLIT (CG = 1): the CTAs of a cluster share a tile's
-// contraction, and the first joins their partial sums.  Warp 0 loads both operands with TMA, warp 1 (of the
-// even CTA) issues the MMAs, warps 4-11 read the accumulators (double-buffered
-// in tensor memory) and store the result.
+// contraction, and the first joins their partial sums in their order.
+//
+// Warp 0 loads both operands with TMA, warp 1 (of the even CTA) issues the
+// MMAs, warps 4-11 read the accumulators (double-buffered in tensor memory)
+// and store the result: as matrix fragments, turned through shared memory by
+// stmatrix, so that a lane stores 16 bytes of a row instead of 2.  Stages fill
+// the shared memory that is left: the loads' latency under load is about 3300
+// cycles, six steps of a pair.
 template <int KIND, int BN, int CG, bool SPLIT>
 struct Cfg {
   static constexpr int EPI_WARPS = 8;

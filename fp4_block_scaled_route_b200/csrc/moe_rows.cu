@@ -69,7 +69,9 @@ constexpr int kThreads = 256;
 
 // ---- permute: y[p] = x[token(p)] ------------------------------------------------
 // W warps copy a row, each thread up to kCopies pieces of 16 bytes that are
-// all loaded before the first is stored.
+// all loaded before the first is stored.  Bound by its writes: 4096 tokens of
+// 7168 bf16 to 32768 rows take 115 us on B200, 4.1 TB/s written; a plain fill
+// of as many bytes takes 120.
 constexpr int kCopies = 4;
 template <int W>
 __global__ void __launch_bounds__(kThreads) permute_kernel(const PermuteParams p) {
@@ -121,7 +123,8 @@ struct Raw {
 
 // ---- combine: out[t] = sum_j g[t, j] y[inv[t, j]] (+ the shared expert's row) --
 // One block per token and 256 pieces of 16 bytes of its columns; the rows of
-// kJoint slots are loaded together.
+// kJoint slots are loaded together (one by one: 118 us, together 85 us for
+// 4096 tokens of 8 rows of 7168 bf16 on B200, 6.2 TB/s).
 constexpr int kJoint = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParams p) {
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParam
 // ---- its gradients: W warps per slot ----------------------------------------------
 // One piece of 16 bytes per thread and pass: with four in flight (and a
 // quarter of the warps) 32768 slots of 7168 values took 260 us on B200, with
-// two 224, with one 184.
+// two 224, with one 184 (5.4 TB/s).
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const RowCombineBwdParams p) {
   griddep_wait();
@@ -274,7 +277,8 @@ __device__ __forceinline__ void codes_int8(const Chunk& v, float scale, float to
 }
 
 // W warps per row; a thread keeps its first kKeep chunks between the two
-// passes and reads the others again.
+// passes (maximum, codes) and reads the others again.  8192 rows of 7168 bf16:
+// 37 us on B200, 4.8 TB/s.
 constexpr int kKeep = 4;
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) quant_int8_kernel(const QuantInt8Params p) {
