@@ -18,9 +18,9 @@
 // moves 64 KB into shared memory per step where two CTAs alone move 96, and
 // the L2 delivers little more than that: with a quarter of the loads left out
 // the dense product took 320 us instead of 352.  32 ragged groups of 32768
-// rows, 4096 x 7168: 1643 us, 1.17 PFLOP/s, about 1.1 GHz at 1000 W (the
-// library's dense product of the same size sustains 1.40); dense 8192 rows:
-// 325 us, 1.48 PFLOP/s (310 us).  8-bit: 8192 x 4096 x 7168 159 us, 3.0 POP/s.
+// rows, 4096 x 7168: 1643 us, 1.17 PFLOP/s, about 1.1 GHz at 1000 W (cuBLAS
+// sustains 1.40 on a dense product of that size); dense 8192 rows: 325 us,
+// 1.48 PFLOP/s (cuBLAS 310 us).  8-bit: 8192 x 4096 x 7168 159 us, 3.0 POP/s.
 #include "moe_grouped.cuh"
 
 namespace moe {
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     // many tiles of ragged groups; here each pair takes the next unit just
     // before it needs it, so that neighbours in order are neighbours in time.
     // The even CTA's warp 2 asks the hardware and tells both CTAs.
-    if (hand_out && rank == 0 && team < work.total) {
+    if (hand_out && rank == 0) {
       const uint32_t handed0 = mapa_rank(handed, 0), handed1 = mapa_rank(handed, 1);
       const uint32_t unit1 = mapa_rank(const_cast<const int*>(unit), 1);
       int asked = 0;
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         *v = block >= 0 ? block / 2 : work.total;
         return block >= 0;
       };
-      for (int i = 0;; ++i) {
+      for (int i = 0; team < work.total; ++i) {
         const int b = i & 1;
         if (!mbar_wait_warp(want, (uint32_t)i & 1u, abort) ||
             !mbar_wait_warp(&taken[b], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort))
@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         __syncwarp();
         if (v >= work.total) break;
       }
-      // the clusters past the last unit need not start at all
+      // the clusters past the last unit need not start at all (each would set
+      // up and leave: offsets that cover few of the rows, or none, leave many)
       for (int v; left;) left = ask(&v);
       // (an answer still on its way lands before the CTA leaves)
       if (*abort && asked) mbar_drain(answered, (uint32_t)(asked - 1) & 1u);

@@ -531,6 +531,70 @@ def test_int8_sums_fill_32_bits():
     check_int8(y, int8_64(q, one[:3], w[None], one[None], torch.tensor([0, 3])), FP32)
 
 
+def test_int8_row_without_a_finite_scale():
+    """A row that held an infinity or a NaN has scale NaN and zero codes: its products are NaN, the others' are not."""
+    x = torch.randn(9, 160, device="cuda").to(FP16)
+    x[3, 7] = float("inf")
+    x[8, 0] = float("nan")
+    q, s = moe.quant_int8(x)
+    w = torch.randint(-128, 128, (40, 160), device="cuda", dtype=torch.int8)
+    c = torch.ones(40, device="cuda")
+    y = moe.int8_gemm(q, s, w, c)
+    assert torch.isnan(y[[3, 8]]).all()
+    keep = [0, 1, 2, 4, 5, 6, 7]
+    check_int8(y[keep], int8_64(q, s, w[None], c[None], torch.tensor([0, 9]))[keep], BF16)
+
+
+def test_groups_that_cover_few_of_many_rows():
+    """Most of the launch's room for tiles stays unused: one small group, or none, in many rows."""
+    P, E, N, K = 60000, 4, 1032, 2056
+    gen = torch.Generator("cuda").manual_seed(21)
+    x, w = randn(gen, P, K, dtype=BF16), randn(gen, E, N, K, dtype=BF16)
+    for off in ([100, 100, 400, 407, 407], [0, 0, 0, 0, 0], [P, P, P, P, P]):
+        o = torch.tensor(off, dtype=torch.int32, device="cuda")
+        y = torch.full((P, N), 2.0, dtype=FP32, device="cuda")
+        moe.grouped_gemm(x, w, o, out=y)
+        ref, A = forward64(x[:512], w, o.clamp(max=512))
+        held = slice(off[0], off[-1])
+        check(y[held], ref[held], tol16(ref, A, K, FP32)[held])
+        assert (y[:off[0]] == 2.0).all() and (y[off[-1]:] == 2.0).all()
+
+
+FIRST_CALLS_CAPTURED = """
+import sys
+import torch
+from fp4_block_scaled_route_b200 import moe
+x, w = torch.randn(300, 2056, device="cuda").bfloat16(), torch.randn(3, 264, 2056, device="cuda").bfloat16()
+off = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda")
+perm = torch.arange(300, dtype=torch.int32, device="cuda")
+g = torch.rand(150, 2, device="cuda")
+w8, c = torch.ones(264, 2064, dtype=torch.int8, device="cuda"), torch.ones(264, device="cuda")
+def step():
+    y = moe.grouped_gemm(x, w, off)
+    q, s = moe.quant_int8(x)
+    return (y, moe.grouped_gemm_dgrad(y, w, off), moe.grouped_gemm_wgrad(y, x, off), moe.permute(x, perm, 1),
+            moe.combine(y, perm, g), *moe.combine_backward(y[:150], y, perm, g),
+            moe.int8_gemm(q, s, w8[:, :2056], c))
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+sys.exit(0 if all(torch.equal(a, b) for a, b in zip(out, step())) else 1)
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing that a first call sets up is refused while a stream is being captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_int8_strides_and_rows_outside():
     counts = [3, 0, 40]
     off = offsets_of(counts, 2)
