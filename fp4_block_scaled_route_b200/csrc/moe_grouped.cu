@@ -68,7 +68,7 @@ struct Cfg {
 
 // Row tiles of one group are taken in bands of this many, all features of a
 // band before the next one, so that the CTAs running at one time share their
-// rows and their weights in the L2.
+// rows and their weights in the L2 (bands of 2, 4 and 16: within 2 %).
 constexpr int kBand = 8;
 
 // A contraction of fewer steps (128 bytes each) is not split, and a share
@@ -82,8 +82,10 @@ constexpr int kSplitChunks = 12, kMinChunks = 4;
 constexpr int kFewChunks = 24;
 
 // Units are handed out at run time from this many contraction steps on, when
-// there are several groups; a pair asks for its next unit kAhead steps before
-// it is through loading the present one.
+// there are several groups (32 ragged groups of 32768 rows, 4096 features: 16
+// steps 264 us dealt out and 286 handed out, 112 steps 1844 and 1650; one group
+// of as many rows 1493 either way); a pair asks for its next unit kAhead steps
+// before it is through loading the present one.
 constexpr int kHandOutChunks = 32;
 constexpr int kAhead = 12;
 
@@ -562,19 +564,29 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
 }  // namespace
 
 GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
-  // Rows a tile should hold: the group's when there is one, else twice the
-  // average, since routed groups vary.
-  const long long want = p.E == 1 ? p.P : 2LL * ((p.P + p.E - 1) / p.E);
   const int chunks = (p.R + (kind == GG_INT8 ? 127 : 63)) / (kind == GG_INT8 ? 128 : 64);
   const long long groups = p.E < p.P ? p.E : p.P;  // that can have rows
-  // most tiles there can be: one for each group with rows, one for each full tile
+  // most tiles there can be: ceil(c / rows) <= 1 + (c - 1) / rows in every group with c rows
   auto most = [&](int rows, int features) {
-    return (groups + p.P / rows) * (long long)((p.M + features - 1) / features);
+    return (groups + (p.P - groups) / rows) * (long long)((p.M + features - 1) / features);
   };
-  GroupedTile t{want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 256, 1, 1, sms, sms};
-  // Few tiles of 64 rows: shared contractions instead of pairs on a few SMs.
-  if (t.rows == 256 && most(64, 128) * 2 <= sms && chunks >= kFewChunks) t.rows = 64;
-  if (t.rows == 256) {
+  // Few tiles: 2 to 8 CTAs share a tile's contraction while every share keeps
+  // kMinChunks steps and all clusters, one for each tile, are resident at once.
+  auto shares = [&](int rows) {
+    int split = 1;
+    while (chunks >= kSplitChunks && split < (rows <= 32 ? 8 : 4) &&
+           most(rows, 128) <= resident_clusters(split * 2, sms) && chunks >= split * 2 * kMinChunks)
+      split *= 2;
+    return split;
+  };
+  // On one CTA without sharing, tiles have 64 rows; on pairs, 256.  B200, 64
+  // groups, 2048 x 4096 bf16, us with 64 rows, 256 (and 32, 16): 4 rows a group
+  // 157, 170 (162, 163), 24: 158, 177 (163, 211), 48: 162, 180 (204), 64: 182,
+  // 182, 96: 218, 188, 128: 265, 193.
+  const long long average = (p.P + p.E - 1) / p.E;
+  GroupedTile t{64, 1, 1, sms, sms};
+  if (average > 64 && !(chunks >= kFewChunks && shares(64) > 1)) {
+    t.rows = 256;
     t.ctas = 2;
     t.grid = t.running = sms / 2 * 2;
     // a cluster for every unit there can be: tiles, and the pieces of the last wave
@@ -582,31 +594,27 @@ GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
     if (p.E > 1 && chunks >= kHandOutChunks && units * 2 < (1LL << 30)) t.grid = (int)units * 2;
     return t;
   }
-  // Few tiles: share the contraction while every share keeps kMinChunks steps
-  // and all CTAs are resident at once; each cluster then takes one tile.
-  const long long tiles = most(t.rows, 128);
-  const int limit = t.rows <= 32 ? 8 : 4;
-  while (chunks >= kSplitChunks && t.split < limit && tiles <= resident_clusters(t.split * 2, sms) &&
-         chunks >= t.split * 2 * kMinChunks)
-    t.split *= 2;
-  if (t.split > 1) t.grid = (int)tiles * t.split;
+  // Shared tiles hold the group's rows when there is one group, else twice the
+  // average, since routed groups vary; a lower tile leaves room for more stages
+  // (8 rows by 4096 x 4096: 9.6 us in tiles of 16, 15.4 in tiles of 64).
+  const long long want = p.E == 1 ? p.P : 2 * average;
+  const int rows = want <= 16 ? 16 : want <= 32 ? 32 : 64;
+  if ((t.split = shares(rows)) > 1) {
+    t.rows = rows;
+    t.grid = (int)most(rows, 128) * t.split;
+  }
   return t;
 }
 
 template <int KIND>
 static cudaError_t launch_kind(GroupedTile t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& txs,
                                const GroupedParams& p, cudaStream_t s) {
-  const bool split = t.split > 1;
   switch (t.rows) {
-    case 16:
-      return split ? launch<KIND, 16, 1, true>(tw, tx, txs, p, t.grid, s)
-                   : launch<KIND, 16, 1, false>(tw, tx, txs, p, t.grid, s);
-    case 32:
-      return split ? launch<KIND, 32, 1, true>(tw, tx, txs, p, t.grid, s)
-                   : launch<KIND, 32, 1, false>(tw, tx, txs, p, t.grid, s);
+    case 16: return launch<KIND, 16, 1, true>(tw, tx, txs, p, t.grid, s);
+    case 32: return launch<KIND, 32, 1, true>(tw, tx, txs, p, t.grid, s);
     case 64:
-      return split ? launch<KIND, 64, 1, true>(tw, tx, txs, p, t.grid, s)
-                   : launch<KIND, 64, 1, false>(tw, tx, txs, p, t.grid, s);
+      return t.split > 1 ? launch<KIND, 64, 1, true>(tw, tx, txs, p, t.grid, s)
+                         : launch<KIND, 64, 1, false>(tw, tx, txs, p, t.grid, s);
     case 256: return launch<KIND, 256, 2, false>(tw, tx, txs, p, t.grid, s);
   }
   return cudaErrorInvalidValue;

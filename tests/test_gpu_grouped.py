@@ -250,16 +250,19 @@ def test_unusable_offsets_compute_nothing(off):
 # Shapes that reach every way a call is tiled on 148 SMs: rows per tile, shares
 # of the contraction, pairs, pieces of the last wave, units handed out at run time.
 WAYS = {
-    "rows16": ([9, 3], 4000, 136),
     "rows16_split8": ([7], 520, 4160),
     "rows16_split8_at_most": ([16], 1912, 4104),
-    "rows16_split2": ([3, 2, 9], 2056, 1032),
     "rows16_split4": ([3, 0, 9], 1160, 2056),
+    "rows16_split2": ([3, 2, 9], 2056, 1032),
+    "rows32_split4": ([17], 4096, 2056),
     "rows32_split2": ([20, 5, 12, 9], 1032, 1096),
-    "rows32": ([13, 9, 20, 2, 10], 2056, 136),
     "rows64_split4": ([60], 136, 3080),
+    "rows64_split2": ([64], 4232, 1544),
     "rows64_few_large": ([300, 0, 41], 264, 2056),
+    "rows64_short": ([9, 3], 4000, 136),
+    "rows64_many": ([13, 9, 20, 2, 10], 2056, 1992),
     "rows64": ([31, 33, 20, 40], 1032, 328),
+    "rows64_two_tiles": ([1, 100, 0, 130, 5], 2056, 1032),
     "pairs": ([300, 500, 65, 129], 2056, 520),
     "pairs_pieces": ([2048], 1288, 648),
     "pairs_handed_out": ([700, 3, 333, 0, 512, 1100], 2824, 2056),
