@@ -123,15 +123,15 @@ struct Raw {
 
 // ---- combine: out[t] = sum_j g[t, j] y[inv[t, j]] (+ the shared expert's row) --
 // One block per token and 256 pieces of 16 bytes of its columns; the rows of
-// kJoint slots are loaded together (one by one: 118 us, together 85 us for
-// 4096 tokens of 8 rows of 7168 bf16 on B200, 6.2 TB/s).
-constexpr int kJoint = 4;
-template <typename T>
+// J slots are loaded together, all of them up to 4 (4096 tokens of 7168 bf16 on
+// B200, 8 slots: one by one 95 us, 2 together 93, 4 together 88, 6.0 TB/s, 8
+// together 97; 2 slots: 36 with J = 2, 40 with 4; 1 slot: 24 with 1, 33 with 4).
+template <typename T, int J>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int pos[kMaxCombine + kJoint];
-  __shared__ float wt[kMaxCombine + kJoint];
+  __shared__ int pos[kMaxCombine];
+  __shared__ float wt[kMaxCombine];
   __shared__ int s_n;
   const int t = blockIdx.x;
   if (threadIdx.x < 32) {
@@ -166,13 +166,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowCombineParam
     Vec<T> acc;
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i) acc.v[i] = 0.0f;
-    for (int j = 0; j < n; j += kJoint) {
-      Raw<T> r[kJoint];
+    for (int j = 0; j < n; j += J) {
+      Raw<T> r[J];
 #pragma unroll
-      for (int q = 0; q < kJoint; ++q)
+      for (int q = 0; q < J; ++q)
         if (j + q < n) r[q].load(y + pos[j + q] * p.ldy, c, p.H);
 #pragma unroll
-      for (int q = 0; q < kJoint; ++q)
+      for (int q = 0; q < J; ++q)
         if (j + q < n) {
           const float g = wt[j + q];
 #pragma unroll
@@ -363,7 +363,13 @@ cudaError_t quant_int8(const QuantInt8Params& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t row_combine(const RowCombineParams& p, cudaStream_t s) {
-  return launch_cluster<combine_kernel<T>>(dim3(p.T, blocks(p.H, kThreads * Vec<T>::N)), kThreads, 0, 1, s, p);
+  const dim3 grid(p.T, blocks(p.H, kThreads * Vec<T>::N));
+  switch (p.k + p.n_shared) {
+    case 1: return launch_cluster<combine_kernel<T, 1>>(grid, kThreads, 0, 1, s, p);
+    case 2: return launch_cluster<combine_kernel<T, 2>>(grid, kThreads, 0, 1, s, p);
+    case 3: return launch_cluster<combine_kernel<T, 3>>(grid, kThreads, 0, 1, s, p);
+  }
+  return launch_cluster<combine_kernel<T, 4>>(grid, kThreads, 0, 1, s, p);
 }
 
 template <typename T>
