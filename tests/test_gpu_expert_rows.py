@@ -146,6 +146,30 @@ def test_combine_backward(dtype, T, k, E, H, n_shared, drop):
             assert not dg[:, j][~ok].any()
 
 
+def test_combine_gradients_against_differences():
+    """combine is linear in y and in the weights, so central differences of it in fp64 are its gradients."""
+    T, k, E, H = 6, 3, 5, 40
+    _, (_, offsets, perm, inv) = make(T, k, E, drop=True, seed=3)
+    gen = torch.Generator("cuda").manual_seed(9)
+    y, dout = torch.randn(T * k, H, generator=gen, device="cuda"), torch.randn(T, H, generator=gen, device="cuda")
+    g = torch.randn(T, k, generator=gen, device="cuda")
+    dy, dg = moe.combine_backward(dout, y, inv, g)
+    at, ok = inv.view(T, k).long().clamp(min=0), (inv.view(T, k) >= 0).double()
+
+    def loss(yy, gg):
+        return ((gg * ok)[..., None] * yy[at]).sum(1).mul(dout.double()).sum()
+    for p, h in ((0, 0), (3, 39), (int(offsets[-1]) - 1, 17)):
+        d = torch.zeros(T * k, H, dtype=torch.float64, device="cuda")
+        d[p, h] = 0.5
+        diff = float(loss(y.double() + d, g.double()) - loss(y.double() - d, g.double()))
+        assert abs(float(dy[p, h]) - diff) <= 1e-5 * (1 + abs(diff))
+    for t, j in ((0, 0), (2, 1), (5, 2)):
+        d = torch.zeros(T, k, dtype=torch.float64, device="cuda")
+        d[t, j] = 0.5
+        diff = float(loss(y.double(), g.double() + d) - loss(y.double(), g.double() - d))
+        assert abs(float(dg[t, j]) - diff) <= 1e-5 * (1 + abs(diff))
+
+
 @TYPES
 def test_row_strides_and_odd_widths(dtype):
     T, k, E, H = 13, 3, 6, 37
