@@ -492,11 +492,15 @@ def _dtype_code(dtype, what):
     raise ValueError(f"{what}: type {dtype} is not supported")
 
 
-def _new_rows(rows, n, dtype, dev):
-    """An unset [rows, n] matrix whose row stride is a multiple of 16 bytes (contiguous where n allows it)."""
+def _rows_out(out, rows, n, dtype, dev, what, name="out"):
+    """(matrix, row stride): `out`, checked, or an unset [rows, n] matrix whose row stride is a multiple of 16 bytes
+    (contiguous where n allows it)."""
+    if out is not None:
+        return out, _matrix(out, rows, n, what, name)
     import torch
     step = 16 // dtype.itemsize
-    return torch.empty_strided((rows, n), (-(-n // step) * step, 1), dtype=dtype, device=dev)
+    ld = -(-n // step) * step
+    return torch.empty_strided((rows, n), (ld, 1), dtype=dtype, device=dev), ld
 
 
 def _matrix(t, rows, cols, what, name):
@@ -555,10 +559,11 @@ def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, statu
     _on(what, dev, "status", status, torch.int32)
 
     def body(s):
-        y = _new_rows(P, M, out_dtype, dev) if out is None else out
-        ldy = _matrix(y, P, M, what, "out")
-        _check(entry(dt, odt, E, P, N, K, offsets.data_ptr(), rows.data_ptr(), ld, w.data_ptr(), ldw, sw, y.data_ptr(),
-                     ldy, _ptr(status), s), entry.__name__)
+        y, ldy = _rows_out(out, P, M, out_dtype, dev, what)
+        st = getattr(lib(), entry)(dt, odt, E, P, N, K, offsets.data_ptr(), rows.data_ptr(), ld, w.data_ptr(), ldw, sw,
+                                   y.data_ptr(), ldy, _ptr(status), s)
+        if st != MOE_OK:
+            raise MoeError(st, entry)
         return y
     return _call(what, dev, stream, body)
 
@@ -569,12 +574,12 @@ def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=No
     x [P, K] and w [E, N, K] bf16 or fp16 with contiguous rows (any row and expert strides that are multiples of 16
     bytes), offsets device int32 [E+1]; out [P, N] in the same type or fp32.  Rows outside every group are left as
     they were (unspecified in an `out` made here).  status: optional device int32, see moe.h."""
-    return _grouped(moe_grouped_gemm, "grouped_gemm", "x", x, True, w, offsets, out, out_dtype, status, stream)
+    return _grouped("moe_grouped_gemm", "grouped_gemm", "x", x, True, w, offsets, out, out_dtype, status, stream)
 
 
 def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, status=None, stream=None):
     """dx[p] = dy[p] w[e], the gradient of grouped_gemm for x (moe_grouped_gemm_dgrad): dy [P, N] -> [P, K]."""
-    return _grouped(moe_grouped_gemm_dgrad, "grouped_gemm_dgrad", "dy", dy, False, w, offsets, out, out_dtype, status,
+    return _grouped("moe_grouped_gemm_dgrad", "grouped_gemm_dgrad", "dy", dy, False, w, offsets, out, out_dtype, status,
                     stream)
 
 
@@ -601,8 +606,8 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
 
     def body(s):
         dw = torch.empty((E, N, K), dtype=out_dtype, device=dev) if out is None else out
-        _check(moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, _ptr(offsets), _ptr(dy), lddy, _ptr(x), ldx, _ptr(dw),
-                                      _ptr(status), s), "moe_grouped_gemm_wgrad")
+        _check(lib().moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(),
+                                            ldx, dw.data_ptr(), _ptr(status), s), "moe_grouped_gemm_wgrad")
         return dw
     return _call(what, dev, stream, body)
 
@@ -625,11 +630,11 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
         _vector(perm, rows, what, "perm")
 
     def body(s):
-        q = _new_rows(rows, K, torch.int8, dev) if out is None else out
+        q, ldq = _rows_out(out, rows, K, torch.int8, dev, what)
         sc = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=dev) if scale is None else scale
         _vector(sc, rows, what, "scale")
-        _check(moe_quant_int8(dt, rows, K, T, k, _ptr(x), ldx, _ptr(perm), _ptr(q),
-                              _matrix(q, rows, K, what, "out"), _ptr(sc), s), "moe_quant_int8")
+        _check(lib().moe_quant_int8(dt, rows, K, T, k, x.data_ptr(), ldx, _ptr(perm), q.data_ptr(), ldq,
+                                    sc.data_ptr(), s), "moe_quant_int8")
         return q, sc
     return _call(what, dev, stream, body)
 
@@ -664,10 +669,9 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
     _on(what, dev, "status", status, torch.int32)
 
     def body(s):
-        y = _new_rows(P, N, out_dtype, dev) if out is None else out
-        _check(moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), _ptr(q), ldq, _ptr(q_scale), _ptr(w), ldw, sw,
-                             _ptr(w_scale), _ptr(y), _matrix(y, P, N, what, "out"), _ptr(status), s),
-               "moe_int8_gemm")
+        y, ldy = _rows_out(out, P, N, out_dtype, dev, what)
+        _check(lib().moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), q.data_ptr(), ldq, q_scale.data_ptr(), w.data_ptr(),
+                                   ldw, sw, w_scale.data_ptr(), y.data_ptr(), ldy, _ptr(status), s), "moe_int8_gemm")
         return y
     return _call(what, dev, stream, body)
 
@@ -688,9 +692,9 @@ def permute(x, perm, k, out=None, stream=None):
     _on(what, dev, "out", out, x.dtype)
 
     def body(s):
-        y = _new_rows(rows, H, x.dtype, dev) if out is None else out
-        _check(moe_permute(dt, rows, H, T, k, _ptr(x), ldx, _ptr(perm), _ptr(y),
-                           _matrix(y, rows, H, what, "out"), s), "moe_permute")
+        y, ldy = _rows_out(out, rows, H, x.dtype, dev, what)
+        _check(lib().moe_permute(dt, rows, H, T, k, x.data_ptr(), ldx, perm.data_ptr(), y.data_ptr(), ldy, s),
+               "moe_permute")
         return y
     return _call(what, dev, stream, body)
 
@@ -726,9 +730,9 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
     _on(what, dev, "out", out, y.dtype)
 
     def body(s):
-        o = _new_rows(T, H, y.dtype, dev) if out is None else out
-        _check(moe_combine(dt, rows, H, T, k, n_shared, _ptr(y), ldy, _ptr(inv), _ptr(topk_w), _ptr(o),
-                           _matrix(o, T, H, what, "out"), s), "moe_combine")
+        o, ldo = _rows_out(out, T, H, y.dtype, dev, what)
+        _check(lib().moe_combine(dt, rows, H, T, k, n_shared, y.data_ptr(), ldy, inv.data_ptr(), _ptr(topk_w),
+                                 o.data_ptr(), ldo, s), "moe_combine")
         return o
     return _call(what, dev, stream, body)
 
@@ -752,11 +756,11 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     _on(what, dev, "dtopk_w", dtopk_w, torch.float32)
 
     def body(s):
-        gy = _new_rows(rows, H, y.dtype, dev) if dy is None else dy
+        gy, lddy = _rows_out(dy, rows, H, y.dtype, dev, what, "dy")
         gw = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=dev) if dtopk_w is None else dtopk_w
         _vector(gw, T * k, what, "dtopk_w")
-        _check(moe_combine_backward(dt, rows, H, T, k, n_shared, _ptr(dout), ldd, _ptr(y), ldy, _ptr(inv),
-                                    _ptr(topk_w), _ptr(gy), _matrix(gy, rows, H, what, "dy"), _ptr(gw), s),
+        _check(lib().moe_combine_backward(dt, rows, H, T, k, n_shared, dout.data_ptr(), ldd, y.data_ptr(), ldy,
+                                          inv.data_ptr(), topk_w.data_ptr(), gy.data_ptr(), lddy, gw.data_ptr(), s),
                "moe_combine_backward")
         return gy, gw
     return _call(what, dev, stream, body)
