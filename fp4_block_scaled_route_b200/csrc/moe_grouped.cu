@@ -230,6 +230,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   const int kb0 = SPLIT ? (int)((long long)chunks * rank / split) : 0;
   const int kb1 = SPLIT ? (int)((long long)chunks * (rank + 1) / split) : chunks;
 
+  // contraction steps that one accumulator takes
+  const int seg = KIND != GG_INT8 && p.out_type == MOE_DT_FP32 ? kSegment : chunks;
+
   // The unit after u, for each warp that walks the units.
   const uint32_t taken0 = CG == 2 ? mapa_rank(taken, 0) : 0;
   int hand = 0;
@@ -330,16 +333,23 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         }
         const int n = (t.rows + 16 * CG - 1) & ~(16 * CG - 1);
         const uint32_t idesc = p.idesc | (uint32_t)(n >> 3) << 17;
-        const int buf = j & 1;
-        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-        if (!ok) break;
-        tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
+        int buf = 0, left = 0;  // the accumulator, and the steps that it still takes
+        for (int kb = kb0; kb < kb1; ++kb, --left) {
+          const bool first = left == 0;
+          if (first) {
+            if (kb != kb0) mma_commit_all<CG>(tfull0 + 8u * buf);
+            buf = j & 1;
+            left = seg;
+            ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
+            if (!ok) break;
+            tc_fence_after();
+            ++j;
+          }
           ok = mbar_wait_warp(&full[st], ph, abort);
           if (!ok) break;
           tc_fence_after();
           const uint64_t off = st * (C::STAGE >> 4);
-          mma_steps4<KIND == GG_INT8, CG>(tmem + buf * BN, ad0 + off, bd0 + off, step_a, step_b, idesc, kb != kb0);
+          mma_steps4<KIND == GG_INT8, CG>(tmem + buf * BN, ad0 + off, bd0 + off, step_a, step_b, idesc, !first);
           mma_commit_all<CG>(empty0 + 8u * st);
           if (++st == STAGES) {
             st = 0;
@@ -353,7 +363,6 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
           u = next_unit(u);
           if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
         }
-        ++j;
       }
       mma_commit_all<CG>(smem_u32(done));
       mbar_drain(done, 0);
@@ -422,7 +431,6 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     for (int u = team; u < work.total && ok; u = next_unit(u)) {
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       if (t.rows <= 0) continue;
-      const int buf = j & 1;
       const int m0 = t.m0 + (CG == 2 ? (int)rank * 128 : 0) + q * 32;  // this warp's first feature
       // int8: the scales of the features this thread holds
       float cs[4];
@@ -439,105 +447,158 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         return KIND == GG_INT8 && lane < C::CB && c + lane < t.rows ? __ldg(p.row_scale + t.p0 + c + lane) : 0.0f;
       };
       float next_scale = scale_of(half * C::CB);
-      ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
-      // the other CTAs' sums have arrived (data written by them: acquire)
-      if (SPLIT && rank == 0) {
-        ok = mbar_wait_cluster(joined, 0, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-      }
-      for (int c0 = half * C::CB; c0 < t.rows && m0 < p.M; c0 += 2 * C::CB) {
-        const int left = t.rows - c0;  // rows of this step: min(left, CB)
-        uint32_t f[2][NG * 4];
-        tmem_ld_16x256b<NG>(acc + c0, f[0]);
-        tmem_ld_16x256b<NG>(acc + (16u << 16) + c0, f[1]);
-        tmem_wait_ld();
-        if (SPLIT) {
-          uint32_t* at = join + (warp - 4) * PER_WARP + (c0 / (2 * C::CB)) * (NG * 8 * 32) + lane * 4;
-          if (rank != 0) {
-            const uint32_t to = mapa_rank(at + (rank - 1) * PER_CTA, 0);
+      // Pairs into fp32: the segments of the contraction add up in registers, a
+      // lane holding one feature of all the warp's rows, so that a store is
+      // 128 bytes of one row.  (32768 ragged rows
+      // of 32 experts, 7168 -> 4096: 1777 us; 2290 when the segments add up in
+      // the result's memory; 1757 with one segment.)
+      if (STEPS > 1 && KIND != GG_INT8 && p.out_type == MOE_DT_FP32) {
+        float s[STEPS][C::CB];
 #pragma unroll
-            for (int i = 0; i < NG * 2; ++i) {
-              const uint32_t* v = &f[i / NG][(i % NG) * 4];
-              st_cluster_v4(to + i * 512, v[0], v[1], v[2], v[3]);
-            }
-            continue;
-          }
-          // in the CTAs' order, whatever order they finished in
-          for (int r = 0; r < split - 1; ++r) {
+        for (int i = 0; i < STEPS * C::CB; ++i) s[i / C::CB][i % C::CB] = 0.0f;
+        for (int left_kb = kb1 - kb0; left_kb > 0; left_kb -= seg, ++j) {
+          const int buf = j & 1;
+          ok = mbar_wait_warp(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
 #pragma unroll
-            for (int i = 0; i < NG * 2; ++i) {
-              const uint4 o = *reinterpret_cast<const uint4*>(at + r * PER_CTA + i * 128);
-              uint32_t* v = &f[i / NG][(i % NG) * 4];
-              v[0] = add_as<KIND>(v[0], o.x);
-              v[1] = add_as<KIND>(v[1], o.y);
-              v[2] = add_as<KIND>(v[2], o.z);
-              v[3] = add_as<KIND>(v[3], o.w);
-            }
+          for (int i = 0; i < STEPS * C::CB; i += 16) {
+            const int c0 = (i / C::CB * 2 + half) * C::CB + i % C::CB;
+            if (c0 >= t.rows) continue;
+            float v[16];
+            tmem_ld16(acc + c0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s[i / C::CB][i % C::CB + k] += v[k];
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
         }
-        const float row_scale = next_scale;
-        next_scale = scale_of(c0 + 2 * C::CB);
-        const bool bf = p.out_type == MOE_DT_BF16;
+        if (!ok) break;
+        float* y = static_cast<float*>(p.y) + (size_t)t.p0 * p.ldy + m0 + lane;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          uint32_t w[4];
-          float rs[2];
-          if (KIND == GG_INT8) {
+        for (int i = 0; i < STEPS * C::CB; ++i) {
+          const int c = (i / C::CB * 2 + half) * C::CB + i % C::CB;
+          if (c < t.rows && m0 + lane < p.M) y[(size_t)c * p.ldy] = s[i / C::CB][i % C::CB];
+        }
+        continue;
+      }
+      // The segments (one, but for long contractions into fp32) add up in
+      // registers: tiles with several steps have left above.
+      uint32_t f[2][NG * 4];
+      for (int left_kb = kb1 - kb0, sg = 0; left_kb > 0; left_kb -= seg, ++sg, ++j) {
+        const bool last = left_kb <= seg;
+        const int buf = j & 1;
+        ok = mbar_wait_warp(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
+        // the other CTAs' sums have arrived (data written by them: acquire)
+        if (SPLIT && rank == 0 && last) {
+          ok = mbar_wait_cluster(joined, 0, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+        }
+        for (int c0 = half * C::CB; c0 < t.rows && m0 < p.M; c0 += 2 * C::CB) {
+          const int left = t.rows - c0;  // rows of this step: min(left, CB)
+          if (STEPS == 1 && sg > 0) {
+            uint32_t h[2][NG * 4];
+            tmem_ld_16x256b<NG>(acc + c0, h[0]);
+            tmem_ld_16x256b<NG>(acc + (16u << 16) + c0, h[1]);
+            tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) rs[h] = __shfl_sync(0xFFFFFFFFu, row_scale, i * 8 + (lane & 3) * 2 + h);
+            for (int i = 0; i < NG * 8; ++i)
+              f[i / (NG * 4)][i % (NG * 4)] = add_as<KIND>(f[i / (NG * 4)][i % (NG * 4)], h[i / (NG * 4)][i % (NG * 4)]);
+          } else {
+            tmem_ld_16x256b<NG>(acc + c0, f[0]);
+            tmem_ld_16x256b<NG>(acc + (16u << 16) + c0, f[1]);
+            tmem_wait_ld();
           }
+          if (STEPS == 1 && !last) continue;
+          if (SPLIT) {
+            uint32_t* at = join + (warp - 4) * PER_WARP + (c0 / (2 * C::CB)) * (NG * 8 * 32) + lane * 4;
+            if (rank != 0) {
+              const uint32_t to = mapa_rank(at + (rank - 1) * PER_CTA, 0);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {  // features 8 g .. 8 g + 7 of the warp's 32
-            float a = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2]);
-            float b = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2 + 1]);
+              for (int i = 0; i < NG * 2; ++i) {
+                const uint32_t* v = &f[i / NG][(i % NG) * 4];
+                st_cluster_v4(to + i * 512, v[0], v[1], v[2], v[3]);
+              }
+              continue;
+            }
+            // in the CTAs' order, whatever order they finished in
+            for (int r = 0; r < split - 1; ++r) {
+#pragma unroll
+              for (int i = 0; i < NG * 2; ++i) {
+                const uint4 o = *reinterpret_cast<const uint4*>(at + r * PER_CTA + i * 128);
+                uint32_t* v = &f[i / NG][(i % NG) * 4];
+                v[0] = add_as<KIND>(v[0], o.x);
+                v[1] = add_as<KIND>(v[1], o.y);
+                v[2] = add_as<KIND>(v[2], o.z);
+                v[3] = add_as<KIND>(v[3], o.w);
+              }
+            }
+          }
+          const float row_scale = next_scale;
+          next_scale = scale_of(c0 + 2 * C::CB);
+          const bool bf = p.out_type == MOE_DT_BF16;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            uint32_t w[4];
+            float rs[2];
             if (KIND == GG_INT8) {
-              a = __fmul_rn(__fmul_rn((float)__float_as_int(a), rs[0]), cs[g]);
-              b = __fmul_rn(__fmul_rn((float)__float_as_int(b), rs[1]), cs[g]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) rs[h] = __shfl_sync(0xFFFFFFFFu, row_scale, i * 8 + (lane & 3) * 2 + h);
             }
-            if (p.out_type == MOE_DT_FP32) {
-              // eight neighbouring lanes (l / 4) fill a 32-byte sector of one row
-              const int m = m0 + g * 8 + (lane >> 2), c = i * 8 + (lane & 3) * 2;
-              float* y = static_cast<float*>(p.y) + (size_t)(t.p0 + c0 + c) * p.ldy + m;
-              if (m < p.M && c < left) y[0] = a;
-              if (m < p.M && c + 1 < left) y[p.ldy] = b;
-            } else {
-              w[g] = pack16(a, b, bf);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {  // features 8 g .. 8 g + 7 of the warp's 32
+              float a = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2]);
+              float b = __uint_as_float(f[g >> 1][i * 4 + (g & 1) * 2 + 1]);
+              if (KIND == GG_INT8) {
+                a = __fmul_rn(__fmul_rn((float)__float_as_int(a), rs[0]), cs[g]);
+                b = __fmul_rn(__fmul_rn((float)__float_as_int(b), rs[1]), cs[g]);
+              }
+              if (p.out_type == MOE_DT_FP32) {
+                // eight neighbouring lanes (l / 4) fill a 32-byte sector of one row
+                const int m = m0 + g * 8 + (lane >> 2), c = i * 8 + (lane & 3) * 2;
+                float* y = static_cast<float*>(p.y) + (size_t)(t.p0 + c0 + c) * p.ldy + m;
+                if (m < p.M && c < left) y[0] = a;
+                if (m < p.M && c + 1 < left) y[p.ldy] = b;
+              } else {
+                w[g] = pack16(a, b, bf);
+              }
             }
+            if (p.out_type == MOE_DT_FP32) continue;
+            stmatrix_x4_trans(turn_st + i * 8 * 80, w[0], w[1], w[2], w[3]);
           }
           if (p.out_type == MOE_DT_FP32) continue;
-          stmatrix_x4_trans(turn_st + i * 8 * 80, w[0], w[1], w[2], w[3]);
-        }
-        if (p.out_type == MOE_DT_FP32) continue;
-        __syncwarp();
-        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(t.p0 + c0) * p.ldy + m0;
+          __syncwarp();
+          uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(t.p0 + c0) * p.ldy + m0;
 #pragma unroll
-        for (int i = 0; i < C::CB / 8; ++i) {
-          const int c = i * 8 + (lane >> 2), part = (lane & 3) * 8;
-          if (c < left && m0 + part < p.M) {
-            const uint4 v = *reinterpret_cast<const uint4*>(turn + c * 80 + part * 2);
-            uint16_t* to = y + c * p.ldy + part;
-            if (m0 + part + 8 <= p.M) {
-              *reinterpret_cast<uint4*>(to) = v;
-            } else {
-              const uint16_t* x = reinterpret_cast<const uint16_t*>(&v);
+          for (int i = 0; i < C::CB / 8; ++i) {
+            const int c = i * 8 + (lane >> 2), part = (lane & 3) * 8;
+            if (c < left && m0 + part < p.M) {
+              const uint4 v = *reinterpret_cast<const uint4*>(turn + c * 80 + part * 2);
+              uint16_t* to = y + c * p.ldy + part;
+              if (m0 + part + 8 <= p.M) {
+                *reinterpret_cast<uint4*>(to) = v;
+              } else {
+                const uint16_t* x = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (m0 + part + k < p.M) to[k] = x[k];
+                for (int k = 0; k < 8; ++k)
+                  if (m0 + part + k < p.M) to[k] = x[k];
+              }
             }
           }
+          __syncwarp();
         }
+        tc_fence_before();
         __syncwarp();
+        if (SPLIT && rank != 0 && last && lane == 0) mbar_arrive_at(mapa_rank(joined, 0));
+        if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (SPLIT && rank != 0 && lane == 0) mbar_arrive_at(mapa_rank(joined, 0));
-      if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
-      ++j;
     }
   }
   tc_fence_before();

@@ -102,6 +102,14 @@ __host__ __device__ constexpr uint32_t idesc_s8(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The tensor cores truncate each addition to an accumulator, about 1.5e-8 of
+// the sum per MMA (6.6e-6 in the 2-norm at a contraction of 7168).  16-bit
+// outputs round that away.  For fp32 outputs an accumulator takes kSegment
+// stages at most, and the segments' sums are added with rounding: 1e-6 at most
+// for contractions up to 16384.  At 32 stages it is twice that, for 1 % of the
+// time of a product and 2 % of an input gradient.
+constexpr int kSegment = 16;
+
 // ---- issue ----------------------------------------------------------------------
 // The issuing warps run their loops with all 32 lanes (so that addresses and
 // descriptors stay in uniform registers) and let one elected lane issue.

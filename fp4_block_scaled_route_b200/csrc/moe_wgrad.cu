@@ -4,7 +4,7 @@
 // What bounds it: for long groups the tensor cores and the loads that feed
 // them (dense, 8192 rows into 4096 x 7168: 343 us, 1.40 PFLOP/s; cuBLAS
 // 342 us), for groups of a few hundred rows also the result's way out
-// (32 groups of 512 rows into 2048 x 7168 bf16, 940 MB: 532 us; 490 us without
+// (32 groups of 512 rows into 2048 x 7168 bf16, 940 MB: 532 us; 432 us without
 // the stores), for short ones that alone (64 groups of 16 rows into 392 x 1032
 // fp32, 104 MB: 37 us, 2.9 TB/s; a plain fill reaches 3.9).
 #include <type_traits>
@@ -41,6 +41,60 @@ struct WCfg {
   static constexpr int MAX_E = (232448 - SMEM) / 4 - 1;
   static_assert((4 * STAGES + 7) * 8 + 8 <= BARS && MAX_E > 0, "shared memory");
 };
+
+// An epilogue warp stores 32 rows of 128 bytes by TMA: v is a lane's row, k and
+// n the first column and row.  Columns and rows past the ends are not written.
+__device__ __forceinline__ void store_box(const CUtensorMap& tmO, uint8_t* box, const uint32_t* v, int k, int n, int e) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* line = box + lane * 128;  // 16-byte piece i of a line sits at i ^ (lane & 7)
+  tma_store_wait_read<0>();          // lane 0's store has read the box
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(line + ((i ^ (lane & 7)) * 16)) =
+        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) tma_store_3d(&tmO, box, k, n, e, policy_evict_normal());
+}
+
+// A warp's part of a tile into fp32 of a group of `rows` rows: the segments add
+// up in 128 registers, then 32 rows n by `wide` columns k leave.  Returns the
+// accumulators read, -1 when a wait gave up.
+__device__ __forceinline__ int sum_tile(const CUtensorMap& tmO, uint32_t acc, int wide, int rows, int j, uint64_t* tfull,
+                                        uint32_t tempty0, volatile int* abort, uint8_t* box, int k0, int cols, int n,
+                                        int e) {
+  float sum[4][32];
+#pragma unroll
+  for (int i = 0; i < 128; ++i) sum[i / 32][i % 32] = 0.0f;
+  int taken = 0;
+  for (; rows > 0; rows -= kSegment * 64, ++taken) {
+    const int buf = (j + taken) & 1;
+    if (!mbar_wait_warp(&tfull[buf], (uint32_t)((j + taken) >> 1) & 1u, abort)) return -1;
+    tc_fence_after();
+#pragma unroll
+    for (int i = 0; i < 128; i += 16) {
+      if (i >= wide) continue;
+      float v[16];
+      tmem_ld16(acc + buf * 256 + i, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum[i / 32][i % 32 + k] += v[k];
+    }
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_at(tempty0 + 8u * buf);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i * 32 >= wide || i * 32 >= cols) continue;
+    uint32_t v[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(sum[i][k]);
+    store_box(tmO, box, v, k0 + i * 32, n, e);
+  }
+  return taken;
+}
 
 // Work of one pair: all features of an expert before the next column of
 // tiles, all tiles of an expert before the next expert.  The units of the
@@ -104,12 +158,26 @@ struct WWalk {
 // SPLIT: p.split pairs of a cluster share a tile's rows; each then sends the
 // others their part of the columns of its sums, adds up its own part in the
 // pairs' order, and stores it.
-template <int STAGES, bool SPLIT>
+//
+// SUM: for long groups into fp32.  A group's segments (see kSegment) add up in
+// the epilogue's registers, for which the other warps leave some of theirs.
+// 8192 rows into 2048 x 7168: 228 us (1.06 PFLOP/s), 277 when the segments add
+// up in the result's memory, 223 with one segment (and 7e-6 off).  Groups of 512
+// rows: 635 us against 690, as their accumulators are free before they leave.
+// Below one segment of rows in all, W_WHOLE: 64 groups of 1100 rows in all into
+// 392 x 1032 take 42.1 us here, 41.5 there.
+enum WMode { W_WHOLE, W_SPLIT, W_SUM };
+constexpr int kSumRegs = 168, kSumRegsLow = 104, kSumRegsHigh = 200;  // at launch; warps 0-3; warps 4-11
+static_assert(128 * kSumRegsLow + 256 * kSumRegsHigh <= 384 * kSumRegs, "registers of the launch");
+
+template <int STAGES, WMode MODE>
 __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                  const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmY16,
                  const __grid_constant__ CUtensorMap tmX16, const WgradParams p) {
   using C = WCfg<STAGES>;
+  constexpr bool SPLIT = MODE == W_SPLIT, SUM = MODE == W_SUM;
+  static_assert(C::THREADS == 384, "register split");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out = smem + STAGES * C::STAGE;
@@ -193,6 +261,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   // come by TMA in boxes of 16 rows, the rest by warp 2.
   auto ragged = [](int held) { return held < C::CH && (held & 15); };
 
+  constexpr int seg = SUM ? kSegment : 1 << 30;  // stages that one accumulator takes
+  if (SUM && warp < 4) regs_shrink<kSumRegsLow>();
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
     const uint32_t full0 = mapa_rank(full, even);
@@ -262,11 +332,18 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         continue;
       }
       const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
-      const int buf = j & 1;
-      ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-      if (!ok) break;
-      tc_fence_after();
-      for (int row = lo; row < hi; row += C::CH) {
+      int buf = 0, left = 0;  // the accumulator, and the stages that it still takes
+      for (int row = lo; row < hi; row += C::CH, --left) {
+        const bool first = left == 0;
+        if (first) {
+          if (row != lo) mma_commit_all<2>(tfull0 + 8u * buf, both);
+          buf = j & 1;
+          left = seg;
+          ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
+          if (!ok) break;
+          tc_fence_after();
+          ++j;
+        }
         const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
         ok = mbar_wait_warp(&full[st], ph, abort);
         if (ok && ragged(hi - row)) {
@@ -279,10 +356,10 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         const uint64_t off = st * (C::STAGE >> 4);
         const uint32_t d = tmem + buf * C::BN;
         if (steps == 4) {
-          mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, row != lo);
+          mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, !first);
         } else {
           for (int kk = 0; kk < steps; ++kk)
-            mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != lo) | (kk != 0));
+            mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, !first | (kk != 0));
         }
         mma_commit_all<2>(empty0 + 8u * st, both);
         if (++st == STAGES) {
@@ -293,7 +370,6 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         if (row == lo) more = take(next);
       }
       if (ok) mma_commit_all<2>(tfull0 + 8u * buf, both);
-      ++j;
     }
     mma_commit_all<2>(smem_u32(done), both);
     mbar_drain(done, 0);
@@ -353,15 +429,14 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
+    if (SUM) regs_grow<kSumRegsHigh>();
     // Two warps per quarter of the rows, one for each half of the columns; a
     // step is a box of 32 rows by 128 bytes.
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tempty0 = mapa_rank(tempty, even);
     uint8_t* box = out + (warp - 4) * C::OUT;
-    uint8_t* line = box + lane * 128;  // 16-byte piece i of a line sits at i ^ (lane & 7)
     const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
     const int width = f32 ? 32 : 64;  // columns of a box
-    const uint64_t pol = policy_evict_normal();
     bool ok = true;
     int j = 0;
     WUnit t;
@@ -369,6 +444,13 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
       if (t.k0 >= p.K) continue;
       const int n = t.n0 + rank * 128 + q * 32, wide = 64 * t.nb, k0 = t.k0 + half * wide;
       const bool none = t.hi == t.lo;
+      if (SUM) {
+        const int read = sum_tile(tmO, tmem + ((uint32_t)(q * 32) << 16) + half * wide, wide, t.hi - t.lo, j, tfull,
+                                  tempty0, abort, box, k0, n < p.N ? p.K - k0 : 0, n, t.e);
+        ok = read >= 0;
+        j += read;
+        continue;
+      }
       const int buf = j & 1;
       if (!none) {
         ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
@@ -469,15 +551,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), bf);
         }
-        tma_store_wait_read<0>();  // lane 0's store has read the box
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(line + ((i ^ (lane & 7)) * 16)) =
-              make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tma_store_3d(&tmO, box, k0 + c, n, t.e, pol);
+        store_box(tmO, box, v, k0 + c, n, t.e);
       }
       if (!none) {
         tc_fence_before();
@@ -500,6 +574,17 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   }
 }
 
+// The register split is only safe if the block is launched with the registers
+// that it counts on.
+template <int STAGES>
+bool sum_fits() {
+  static const bool fits = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, wgrad_kernel<STAGES, W_SUM>) == cudaSuccess && fa.numRegs >= kSumRegs;
+  }();
+  return fits;
+}
+
 }  // namespace
 
 cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUtensorMap& to,
@@ -515,14 +600,21 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
   const long long tiles = (long long)p.E * ((p.N + kWM - 1) / kWM) * ((p.K + kWN - 1) / kWN);
   const int stages = (int)((p.P / p.E + 63) / 64);
   p.split = 1;
-  while (p.split < 4 && tiles <= resident_clusters(p.split * 4, sms) && stages >= p.split * 2 * kMinStages)
+  const bool f32 = p.out_type == MOE_DT_FP32;
+  // (into fp32 a share of a group of average length is one segment, see kSegment)
+  const int most = f32 ? 4 * kSegment : 1 << 20;
+  while (p.split < 4 && stages <= most && tiles <= resident_clusters(p.split * 4, sms) && stages >= p.split * 2 * kMinStages)
     p.split *= 2;
   const int grid = p.split > 1 ? (int)tiles * p.split * 2 : sms / 2 * 2;
   auto go = [&](auto n) {
     using C = WCfg<n>;
     const size_t smem = C::SMEM + (p.E + 1) * sizeof(int32_t);
-    return p.split > 1 ? launch_cluster<wgrad_kernel<n, true>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, ty16, tx16, p)
-                       : launch_cluster<wgrad_kernel<n, false>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
+    if (p.split > 1)
+      return launch_cluster<wgrad_kernel<n, W_SPLIT>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, ty16, tx16, p);
+    if (!f32 || p.P <= kSegment * C::CH)  // (no group has a second segment)
+      return launch_cluster<wgrad_kernel<n, W_WHOLE>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
+    if (!sum_fits<n>()) return cudaErrorInvalidConfiguration;
+    return launch_cluster<wgrad_kernel<n, W_SUM>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
   };
   static_assert(WCfg<5>::MAX_E >= 1024, "every expert count has a variant");
   return p.E <= WCfg<6>::MAX_E ? go(std::integral_constant<int, 6>{}) : go(std::integral_constant<int, 5>{});

@@ -296,6 +296,32 @@ def test_every_tiling(way):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 9], [60], [700, 40, 300], [130, 257, 500, 0, 64] * 3], ids=["few", "some", "few_large", "pairs"])
+def test_long_contractions_into_fp32(counts):
+    """fp32 results add up segments of 1024: the truncated additions of a segment, and one rounding per segment."""
+    off = offsets_of(counts)
+    P, E, N, K = sum(counts), len(counts), 1032, 7176
+    gen = torch.Generator("cuda").manual_seed(31)
+    w, x = randn(gen, E, N, K, dtype=BF16), randn(gen, P, K, dtype=BF16)
+    ref, A = forward64(x, w, off)
+    tol = (1024 + 16 + 8) * 2.0 ** -23 * A
+    check(moe.grouped_gemm(x, w, off, out_dtype=FP32), ref, tol)
+    check(moe.grouped_gemm_dgrad(x, w.transpose(1, 2).contiguous(), off, out_dtype=FP32), ref, tol)
+
+
+def test_long_groups_into_fp32():
+    """The same for weight gradients, over groups of many rows and short ones."""
+    for counts, N, K in (([5000, 1, 1030, 0, 2048, 1024], 264, 1160), ([9001], 1800, 2056), ([4096], 136, 200)):
+        off = offsets_of(counts)
+        P = sum(counts)
+        gen = torch.Generator("cuda").manual_seed(32)
+        dy, x = randn(gen, P, N, dtype=BF16), randn(gen, P, K, dtype=BF16)
+        ref, A = wgrad64(dy, x, off)
+        dw = moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)
+        check(dw, ref, (1024 + 16 + 9) * 2.0 ** -23 * A + TINY[FP32])
+        assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32))
+
+
 def test_weight_gradient_tilings():
     """Whole waves of tiles, halves of the last wave, more experts than the larger pipeline has room for, and few tiles
     whose rows two or four pairs share (some of them without any)."""
