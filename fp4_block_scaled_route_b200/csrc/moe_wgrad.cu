@@ -3,10 +3,10 @@
 //
 // What bounds it: for long groups the tensor cores and the loads that feed
 // them (dense, 8192 rows into 4096 x 7168: 343 us, 1.40 PFLOP/s; cuBLAS
-// 342 us), for groups of a few hundred rows also the result's way out
-// (32 groups of 512 rows into 2048 x 7168 bf16, 940 MB: 532 us; 432 us without
-// the stores), for short ones that alone (64 groups of 16 rows into 392 x 1032
-// fp32, 104 MB: 37 us, 2.9 TB/s; a plain fill reaches 3.9).
+// 342 us), for groups of a few hundred rows also the result's way out (32
+// groups of 512 rows into 2048 x 7168 bf16, 940 MB: 498 us), for short ones
+// that alone (64 groups of 16 rows into 392 x 1032 fp32, 104 MB: 37 us, 2.9
+// TB/s; a plain fill reaches 3.9).
 #include <type_traits>
 
 #include "moe_grouped.cuh"
@@ -159,13 +159,10 @@ struct WWalk {
 // others their part of the columns of its sums, adds up its own part in the
 // pairs' order, and stores it.
 //
-// SUM: for long groups into fp32.  A group's segments (see kSegment) add up in
+// SUM: into fp32.  A group's segments (see kSegment) add up in
 // the epilogue's registers, for which the other warps leave some of theirs.
 // 8192 rows into 2048 x 7168: 228 us (1.06 PFLOP/s), 277 when the segments add
-// up in the result's memory, 223 with one segment (and 7e-6 off).  Groups of 512
-// rows: 635 us against 690, as their accumulators are free before they leave.
-// Below one segment of rows in all, W_WHOLE: 64 groups of 1100 rows in all into
-// 392 x 1032 take 42.1 us here, 41.5 there.
+// up in the result's memory, 223 with one segment (and 7e-6 off).
 enum WMode { W_WHOLE, W_SPLIT, W_SUM };
 constexpr int kSumRegs = 168, kSumRegsLow = 104, kSumRegsHigh = 200;  // at launch; warps 0-3; warps 4-11
 static_assert(128 * kSumRegsLow + 256 * kSumRegsHigh <= 384 * kSumRegs, "registers of the launch");
@@ -436,7 +433,6 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     const uint32_t tempty0 = mapa_rank(tempty, even);
     uint8_t* box = out + (warp - 4) * C::OUT;
     const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
-    const int width = f32 ? 32 : 64;  // columns of a box
     bool ok = true;
     int j = 0;
     WUnit t;
@@ -537,21 +533,23 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         break;  // a cluster has one tile
       }
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * wide;
-      for (int c = 0; c < wide && k0 + c < p.K && n < p.N; c += width) {
-        uint32_t v[64];  // (only 32 of fp32)
-        if (none) {
+      // The whole accumulator is read and rounded before anything is stored, so
+      // that the MMAs of the tile after next can start (box by box: 32 groups
+      // of 512 rows 536 us, so 498).
+      uint32_t w[2][32];  // a box of 64 columns each
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t v[64];
+        if (none || b * 64 >= wide) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = 0;
         } else {
-          tmem_ld32(acc + c, reinterpret_cast<float*>(v));
-          if (!f32) tmem_ld32(acc + c + 32, reinterpret_cast<float*>(v) + 32);
+          tmem_ld32(acc + b * 64, reinterpret_cast<float*>(v));
+          tmem_ld32(acc + b * 64 + 32, reinterpret_cast<float*>(v) + 32);
           tmem_wait_ld();
         }
-        if (!f32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), bf);
-        }
-        store_box(tmO, box, v, k0 + c, n, t.e);
+        for (int i = 0; i < 32; ++i) w[b][i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), bf);
       }
       if (!none) {
         tc_fence_before();
@@ -559,6 +557,9 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
         ++j;
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (b * 64 < wide && k0 + b * 64 < p.K && n < p.N) store_box(tmO, box, w[b], k0 + b * 64, n, t.e);
     }
     tma_store_wait_all();
   }
@@ -600,9 +601,8 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
   const long long tiles = (long long)p.E * ((p.N + kWM - 1) / kWM) * ((p.K + kWN - 1) / kWN);
   const int stages = (int)((p.P / p.E + 63) / 64);
   p.split = 1;
-  const bool f32 = p.out_type == MOE_DT_FP32;
   // (into fp32 a share of a group of average length is one segment, see kSegment)
-  const int most = f32 ? 4 * kSegment : 1 << 20;
+  const int most = p.out_type == MOE_DT_FP32 ? 4 * kSegment : 1 << 20;
   while (p.split < 4 && stages <= most && tiles <= resident_clusters(p.split * 4, sms) && stages >= p.split * 2 * kMinStages)
     p.split *= 2;
   const int grid = p.split > 1 ? (int)tiles * p.split * 2 : sms / 2 * 2;
@@ -611,7 +611,7 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
     const size_t smem = C::SMEM + (p.E + 1) * sizeof(int32_t);
     if (p.split > 1)
       return launch_cluster<wgrad_kernel<n, W_SPLIT>>(grid, C::THREADS, smem, 2 * p.split, s, ty, tx, to, ty16, tx16, p);
-    if (!f32 || p.P <= kSegment * C::CH)  // (no group has a second segment)
+    if (p.out_type != MOE_DT_FP32)
       return launch_cluster<wgrad_kernel<n, W_WHOLE>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
     if (!sum_fits<n>()) return cudaErrorInvalidConfiguration;
     return launch_cluster<wgrad_kernel<n, W_SUM>>(grid, C::THREADS, smem, 2, s, ty, tx, to, ty16, tx16, p);
