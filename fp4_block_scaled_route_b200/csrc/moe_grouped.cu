@@ -333,32 +333,28 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         }
         const int n = (t.rows + 16 * CG - 1) & ~(16 * CG - 1);
         const uint32_t idesc = p.idesc | (uint32_t)(n >> 3) << 17;
-        int buf = 0, left = 0;  // the accumulator, and the steps that it still takes
-        for (int kb = kb0; kb < kb1; ++kb, --left) {
-          const bool first = left == 0;
-          if (first) {
-            if (kb != kb0) mma_commit_all<CG>(tfull0 + 8u * buf);
-            buf = j & 1;
-            left = seg;
-            ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-            if (!ok) break;
-            tc_fence_after();
-            ++j;
-          }
-          ok = mbar_wait_warp(&full[st], ph, abort);
+        for (int kb = kb0; kb < kb1; ++j) {  // one accumulator each: segments
+          const int buf = j & 1, first = kb, end = min(kb1, kb + seg);
+          ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t off = st * (C::STAGE >> 4);
-          mma_steps4<KIND == GG_INT8, CG>(tmem + buf * BN, ad0 + off, bd0 + off, step_a, step_b, idesc, !first);
-          mma_commit_all<CG>(empty0 + 8u * st);
-          if (++st == STAGES) {
-            st = 0;
-            ph ^= 1u;
+          for (; kb < end; ++kb) {
+            ok = mbar_wait_warp(&full[st], ph, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t off = st * (C::STAGE >> 4);
+            mma_steps4<KIND == GG_INT8, CG>(tmem + buf * BN, ad0 + off, bd0 + off, step_a, step_b, idesc, kb != first);
+            mma_commit_all<CG>(empty0 + 8u * st);
+            if (++st == STAGES) {
+              st = 0;
+              ph ^= 1u;
+            }
+            // the next tile is looked up while the tensor cores have work
+            if (!hand_out && kb == kb0 && u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
           }
-          // the next tile is looked up while the tensor cores have work
-          if (!hand_out && kb == kb0 && u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
+          if (!ok) break;
+          mma_commit_all<CG>(tfull0 + 8u * buf);
         }
-        if (ok) mma_commit_all<CG>(tfull0 + 8u * buf);
         if (hand_out) {
           u = next_unit(u);
           if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);

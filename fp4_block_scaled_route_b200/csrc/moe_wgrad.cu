@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   // come by TMA in boxes of 16 rows, the rest by warp 2.
   auto ragged = [](int held) { return held < C::CH && (held & 15); };
 
-  constexpr int seg = SUM ? kSegment : 1 << 30;  // stages that one accumulator takes
   if (SUM && warp < 4) regs_shrink<kSumRegsLow>();
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
@@ -329,44 +328,40 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         continue;
       }
       const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
-      int buf = 0, left = 0;  // the accumulator, and the stages that it still takes
-      for (int row = lo; row < hi; row += C::CH, --left) {
-        const bool first = left == 0;
-        if (first) {
-          if (row != lo) mma_commit_all<2>(tfull0 + 8u * buf, both);
-          buf = j & 1;
-          left = seg;
-          ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
-          if (!ok) break;
-          tc_fence_after();
-          ++j;
-        }
-        const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
-        ok = mbar_wait_warp(&full[st], ph, abort);
-        if (ok && ragged(hi - row)) {
-          ok = mbar_wait_cluster(&filled[st], (uses >> st) & 1u, abort);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          uses ^= 1u << st;
-        }
+      for (int row = lo; row < hi; ++j) {  // one accumulator each: segments
+        const int buf = j & 1, first = row, end = SUM ? min(hi, row + kSegment * C::CH) : hi;
+        const uint32_t d = tmem + buf * C::BN;
+        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t off = st * (C::STAGE >> 4);
-        const uint32_t d = tmem + buf * C::BN;
-        if (steps == 4) {
-          mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, !first);
-        } else {
-          for (int kk = 0; kk < steps; ++kk)
-            mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, !first | (kk != 0));
+        for (; row < end; row += C::CH) {
+          const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
+          ok = mbar_wait_warp(&full[st], ph, abort);
+          if (ok && ragged(hi - row)) {
+            ok = mbar_wait_cluster(&filled[st], (uses >> st) & 1u, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            uses ^= 1u << st;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t off = st * (C::STAGE >> 4);
+          if (steps == 4) {
+            mma_steps4<false, 2>(d, ad0 + off, bd0 + off, 128, 128, idesc, row != first);
+          } else {
+            for (int kk = 0; kk < steps; ++kk)
+              mma_f16_pair(d, ad0 + off + 128 * kk, bd0 + off + 128 * kk, idesc, (row != first) | (kk != 0));
+          }
+          mma_commit_all<2>(empty0 + 8u * st, both);
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+          // the next unit is looked up while the tensor cores have work
+          if (row == lo) more = take(next);
         }
-        mma_commit_all<2>(empty0 + 8u * st, both);
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1u;
-        }
-        // the next unit is looked up while the tensor cores have work
-        if (row == lo) more = take(next);
+        if (!ok) break;
+        mma_commit_all<2>(tfull0 + 8u * buf, both);
       }
-      if (ok) mma_commit_all<2>(tfull0 + 8u * buf, both);
     }
     mma_commit_all<2>(smem_u32(done), both);
     mbar_drain(done, 0);
