@@ -247,6 +247,24 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) 
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
+// Bounded wait of a whole warp for what lies any number of units of work away:
+// the limit covers one unit, and starts anew whenever *moved, which the
+// producer advances unit by unit, has changed.
+__device__ __forceinline__ bool mbar_wait_moving(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                 const volatile int* moved) {
+  bool ok = mbar_try_wait(bar, parity);
+  long long t0 = clock64();
+  for (int seen = *moved; !ok && !*abort; ok = mbar_try_wait(bar, parity)) {
+    const int now = *moved;
+    if (now != seen) {
+      seen = now;
+      t0 = clock64();
+    } else if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
 // Bounded wait used while draining: like mbar_wait, but blind to the abort word.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();

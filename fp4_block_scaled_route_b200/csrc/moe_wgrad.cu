@@ -39,7 +39,7 @@ struct WCfg {
   static constexpr int BARS = 512;
   static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * OUT + BARS;  // (+ the offsets)
   static constexpr int MAX_E = (232448 - SMEM) / 4 - 1;
-  static_assert((4 * STAGES + 7) * 8 + 8 <= BARS && MAX_E > 0, "shared memory");
+  static_assert((4 * STAGES + 7) * 8 + 12 <= BARS && MAX_E > 0, "shared memory");
 };
 
 // An epilogue warp stores 32 rows of 128 bytes by TMA: v is a lane's row, k and
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   uint64_t* done = joined + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* moved = abort + 1;  // units that warp 0 has come to
   int* s_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + C::BARS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     }
     mbar_init(done, 1);
     *abort = 0;
+    *moved = 0;
     mbar_fence_init();
     tma_prefetch_map(&tmY);
     tma_prefetch_map(&tmX);
@@ -267,6 +269,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     WUnit t;
     while (ok && take(t)) {
       if (t.k0 >= p.K) continue;
+      if (lane == 0) *moved = *moved + 1;
+      __syncwarp();
       const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 64 * t.nb, nb = t.nb;
       const uint32_t bytes = (2 + nb) * C::BOX;
       for (int row = t.lo; row < t.hi; row += C::CH) {
@@ -405,7 +409,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
           }
         }
       }
-      ok = mbar_wait_warp(&fill[s], (uses >> s) & 1u, abort);
+      // (units without such rows are passed over here, so the first one that has some may be far away)
+      ok = mbar_wait_moving(&fill[s], (uses >> s) & 1u, abort, moved);
       if (!ok) break;
       uses ^= 1u << s;
       uint8_t* a = smem + s * C::STAGE + first * 128;
