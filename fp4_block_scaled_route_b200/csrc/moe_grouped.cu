@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   const int kb1 = SPLIT ? (int)((long long)chunks * (rank + 1) / split) : chunks;
 
   // contraction steps that one accumulator takes
-  const int seg = KIND != GG_INT8 && p.out_type == MOE_DT_FP32 ? kSegment : chunks;
+  const int seg = KIND == GG_INT8 ? chunks : segment_stages(p.out_type);
 
   // The unit after u, for each warp that walks the units.
   const uint32_t taken0 = CG == 2 ? mapa_rank(taken, 0) : 0;
@@ -443,12 +443,12 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         return KIND == GG_INT8 && lane < C::CB && c + lane < t.rows ? __ldg(p.row_scale + t.p0 + c + lane) : 0.0f;
       };
       float next_scale = scale_of(half * C::CB);
-      // Pairs into fp32: the segments of the contraction add up in registers, a
+      // Pairs into fp32, or of several segments: these add up in registers, a
       // lane holding one feature of all the warp's rows, so that a store is
-      // 128 bytes of one row.  (32768 ragged rows
+      // 128 (or 64) bytes of one row.  (Into fp32, 32768 ragged rows
       // of 32 experts, 7168 -> 4096: 1777 us; 2290 when the segments add up in
       // the result's memory; 1757 with one segment.)
-      if (STEPS > 1 && KIND != GG_INT8 && p.out_type == MOE_DT_FP32) {
+      if (STEPS > 1 && KIND != GG_INT8 && (p.out_type == MOE_DT_FP32 || chunks > seg)) {
         float s[STEPS][C::CB];
 #pragma unroll
         for (int i = 0; i < STEPS * C::CB; ++i) s[i / C::CB][i % C::CB] = 0.0f;
@@ -473,16 +473,22 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
           if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
         }
         if (!ok) break;
-        float* y = static_cast<float*>(p.y) + (size_t)t.p0 * p.ldy + m0 + lane;
+        const size_t at = (size_t)t.p0 * p.ldy + m0 + lane;
 #pragma unroll
         for (int i = 0; i < STEPS * C::CB; ++i) {
           const int c = (i / C::CB * 2 + half) * C::CB + i % C::CB;
-          if (c < t.rows && m0 + lane < p.M) y[(size_t)c * p.ldy] = s[i / C::CB][i % C::CB];
+          const float v = s[i / C::CB][i % C::CB];
+          if (c >= t.rows || m0 + lane >= p.M) continue;
+          if (p.out_type == MOE_DT_FP32)
+            static_cast<float*>(p.y)[at + (size_t)c * p.ldy] = v;
+          else
+            static_cast<uint16_t*>(p.y)[at + (size_t)c * p.ldy] = (uint16_t)pack16(v, 0.0f, p.out_type == MOE_DT_BF16);
         }
+        __syncwarp();
         continue;
       }
-      // The segments (one, but for long contractions into fp32) add up in
-      // registers: tiles with several steps have left above.
+      // The segments (one, but for long contractions) add up in registers:
+      // tiles with several steps have left above.
       uint32_t f[2][NG * 4];
       for (int left_kb = kb1 - kb0, sg = 0; left_kb > 0; left_kb -= seg, ++sg, ++j) {
         const bool last = left_kb <= seg;

@@ -102,13 +102,22 @@ __host__ __device__ constexpr uint32_t idesc_s8(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// The tensor cores truncate each addition to an accumulator, about 1.5e-8 of
-// the sum per MMA (6.6e-6 in the 2-norm at a contraction of 7168).  16-bit
-// outputs round that away.  For fp32 outputs an accumulator takes kSegment
-// stages at most, and the segments' sums are added with rounding: 1e-6 at most
-// for contractions up to 16384.  At 32 stages it is twice that, for 1 % of the
-// time of a product and 2 % of an input gradient.
+// The tensor cores truncate each addition to an accumulator, so that its error
+// grows with their number.  An accumulator therefore takes a segment of the
+// contraction, and the segments' sums are added with rounding.  Measured on
+// B200 for terms of one sign, relative to the sum: 64 MMAs of 16 products lose
+// 1.0e-6 (bf16) and 5.8e-6 (fp16, whose products are longer and cut as well),
+// longer segments 1e-7 per MMA of either; with random signs 64 MMAs are off by
+// 1.0e-6 and 1.3e-6 in the 2-norm.
+//   fp32 outputs: segments of 16 stages, 64 MMAs.  With 32 stages twice the
+//     error, for 1 % of the time of a product and 2 % of an input gradient.
+//   fp16: 128 stages, 5e-5, a tenth of half a step (4.9e-4; one accumulator
+//     over 2^18 elements is off by 1.7e-3).
+//   bf16: 512 stages, 1.7e-4, 5 % of half a step (3.9e-3).
 constexpr int kSegment = 16;
+__host__ __device__ constexpr int segment_stages(int out_type) {
+  return out_type == MOE_DT_FP32 ? kSegment : out_type == MOE_DT_FP16 ? 128 : 512;
+}
 
 // ---- issue ----------------------------------------------------------------------
 // The issuing warps run their loops with all 32 lanes (so that addresses and

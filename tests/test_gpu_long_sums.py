@@ -1,0 +1,66 @@
+"""GPU tests of very long contractions, against sums in fp64.
+
+The tensor cores truncate each addition to an accumulator, always towards
+zero, so with terms of one sign the error grows with the number of additions
+and does not average out.  An accumulator therefore takes a bounded number of
+them, and the segments' sums are added with rounding.
+
+Tolerance, for terms of one sign, relative to the sum: an addition takes 16
+products and the accumulator, aligned to the largest of them and cut there at
+24 bits or more, so each loses less than one unit in the last place, 2^-23 of
+the partial sum, and the total as much again when it is cut: 17 + 1 units.  The
+partial sums of a segment grow evenly, so they average half of it, with 2 % for
+the unevenness of random terms.  A segment has 128 steps of 64 elements into
+fp16 (512 additions) and 512 into bf16 (2048 additions): 512 / 2 * 18 * 2^-23 *
+1.02 = 5.6e-4 and 2.2e-3.  The segments' own additions round 128 times at most,
+2^-24 each, and the output once.  (One accumulator over these lengths is off by
+1.5e-3 on fp16.)"""
+import numpy as np
+import pytest
+import torch
+
+from fp4_block_scaled_route_b200 import moe
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+LOSS = {t: n / 2 * 18 * 2.0 ** -23 * 1.02 + 128 * 2.0 ** -24 for t, n in ((FP16, 512), (BF16, 2048))}
+TYPES = pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+
+
+def offsets_of(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+def positive(gen, *shape, dtype, scale=1.0):
+    return ((torch.rand(*shape, generator=gen, device="cuda") + 0.5) * scale).to(dtype)
+
+
+def check(got, ref):
+    """got against ref, whose terms have one sign."""
+    err = ((got.double() - ref) / ref).abs()
+    assert bool((err <= torch.finfo(got.dtype).eps / 2 + LOSS[got.dtype]).all()), float(err.max())
+
+
+# rows of each group, features; by what computes them
+@TYPES
+@pytest.mark.parametrize("counts,M", [([300], 264), ([200, 0, 150], 136), ([40, 1, 70], 6000), ([5], 72), ([50], 200),
+                                      ([300], 2056), ([200, 0, 150], 2056)],
+                         ids=["large_shared", "large_groups_shared", "one_cta", "few_rows_shared", "shared", "pairs",
+                              "pairs_handed_out"])
+def test_long_products(dtype, counts, M):
+    K = 1 << 20 if M < 1000 else 1 << 18
+    off = offsets_of(counts)
+    P, E = sum(counts), len(counts)
+    gen = torch.Generator("cuda").manual_seed(P)
+    x = positive(gen, P, K, dtype=dtype)
+    w = positive(gen, E, M, K, dtype=dtype, scale=2.0 ** -8)
+    ref = torch.cat([x[a:b].double() @ w[e].double().T for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = moe.grouped_gemm(x, w, off, status=status)
+    check(y, ref)
+    assert torch.equal(y, moe.grouped_gemm(x, w, off))
+    wt = w.transpose(1, 2).contiguous()   # the input gradient's contraction runs over w's rows
+    del w
+    check(moe.grouped_gemm_dgrad(x, wt, off, status=status), ref)
+    assert int(status) == 0
