@@ -96,6 +96,17 @@ __device__ __forceinline__ int sum_tile(const CUtensorMap& tmO, uint32_t acc, in
   return taken;
 }
 
+// 16 columns of one accumulator added to another, for this warp's 32 lanes.
+__device__ __forceinline__ void add_columns(uint32_t to, uint32_t from) {
+  float a[16], b[16];
+  tmem_ld16(to, a);
+  tmem_ld16(from, b);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] += b[i];
+  tmem_st16(to, a);
+}
+
 // Work of one pair: all features of an expert before the next column of
 // tiles, all tiles of an expert before the next expert.  The units of the
 // last, partial wave are halves of 128 columns when they still are one wave.
@@ -159,7 +170,12 @@ struct WWalk {
 // others their part of the columns of its sums, adds up its own part in the
 // pairs' order, and stores it.
 //
-// SUM: into fp32.  A group's segments (see kSegment) add up in
+// The segments of a long group (see kSegment) add up in tensor memory: the first
+// keeps its accumulator, the others take turns in the second, and the epilogue
+// adds each to the first.  The MMAs wait meanwhile: 32768 rows into 2048 x 4096
+// fp16, four segments, 372 -> 377 us.
+//
+// SUM: into fp32.  A group's segments add up in
 // the epilogue's registers, for which the other warps leave some of theirs.
 // 8192 rows into 2048 x 7168: 228 us (1.06 PFLOP/s), 277 when the segments add
 // up in the result's memory, 223 with one segment (and 7e-6 off).
@@ -242,6 +258,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
   tc_fence_after();
   griddep_launch_dependents();  // (tensor memory is held: no later kernel can take it first)
   const uint32_t tmem = *tmem_holder;
+  const int seg = segment_stages(p.out_type) * C::CH;  // rows that one accumulator takes
   // (a unit's place in the walk: the same for every role)
   WWalk walk(s_off, bad ? 0 : p.E, p.N, p.K, team, teams);
   // The next unit, with this pair's share of the rows: whole stages of them.
@@ -319,9 +336,8 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     const uint64_t ad0 = sdesc_mn_sw128(smem_u32(smem), C::BOX);
     const uint64_t bd0 = sdesc_mn_sw128(smem_u32(smem) + 2 * C::BOX, C::BOX);
     uint32_t uses = 0;  // parity of each stage's next use of filled
-    uint32_t st = 0, ph = 0;
+    uint32_t st = 0, ph = 0, cur = 0, acc_ph = 0;  // next unit's accumulator; parity of each one's next use
     bool ok = true;
-    int j = 0;
     WUnit next;
     bool more = take(next);
     while (more && ok) {
@@ -332,11 +348,14 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         continue;
       }
       const uint32_t idesc = p.idesc | (uint32_t)(128 * nb >> 3) << 17;
-      for (int row = lo; row < hi; ++j) {  // one accumulator each: segments
-        const int buf = j & 1, first = row, end = SUM ? min(hi, row + kSegment * C::CH) : hi;
+      for (int row = lo; row < hi;) {  // segments
+        const uint32_t buf = SUM || row == lo ? cur : cur ^ 1u;
+        const int first = row, end = min(hi, row + seg);
         const uint32_t d = tmem + buf * C::BN;
-        ok = mbar_wait_warp(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort);
+        ok = mbar_wait_warp(&tempty[buf], ((acc_ph >> buf) & 1u) ^ 1u, abort);
         if (!ok) break;
+        acc_ph ^= 1u << buf;
+        if (SUM) cur ^= 1u;
         tc_fence_after();
         for (; row < end; row += C::CH) {
           const int held = min(C::CH, hi - row), steps = (held + 15) / 16;
@@ -366,6 +385,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         if (!ok) break;
         mma_commit_all<2>(tfull0 + 8u * buf, both);
       }
+      if (!SUM) cur ^= 1u;
     }
     mma_commit_all<2>(smem_u32(done), both);
     mbar_drain(done, 0);
@@ -435,6 +455,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
     const bool f32 = p.out_type == MOE_DT_FP32, bf = p.out_type == MOE_DT_BF16;
     bool ok = true;
     int j = 0;
+    uint32_t cur = 0, acc_ph = 0;  // as in warp 1
     WUnit t;
     while (ok && take(t)) {
       if (t.k0 >= p.K) continue;
@@ -447,12 +468,33 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         j += read;
         continue;
       }
-      const int buf = j & 1;
+      const uint32_t buf = cur, quarter = tmem + ((uint32_t)(q * 32) << 16);
       if (!none) {
-        ok = mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = mbar_wait_warp(&tfull[buf], (acc_ph >> buf) & 1u, abort);
         if (!ok) break;
+        acc_ph ^= 1u << buf;
         tc_fence_after();
+        // the columns that this warp reads, of SPLIT's owners too
+        const int blocks = 4 * t.nb / split;
+        for (int left = t.hi - t.lo - seg; left > 0; left -= seg) {
+          const uint32_t other = buf ^ 1u;
+          ok = mbar_wait_warp(&tfull[other], (acc_ph >> other) & 1u, abort);
+          if (!ok) break;
+          acc_ph ^= 1u << other;
+          tc_fence_after();
+          for (int pr = 0; pr < split; ++pr)
+            for (int b = 0; b < blocks; ++b) {
+              const uint32_t at = quarter + ((2 * pr + half) * blocks + b) * 16;
+              add_columns(at + buf * C::BN, at + other * C::BN);
+            }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(tempty0 + 8u * other);
+          __syncwarp();
+        }
+        if (!ok) break;
+        cur ^= 1u;
       }
       if (SPLIT) {
         // Every pair owns 1 / split of the tile's columns, of which this warp
@@ -461,7 +503,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         // [sender][warp][block][register / 4][lane][4] words.
         const int part = 128 * t.nb / split, blocks = part / 32;
         uint32_t* sums = reinterpret_cast<uint32_t*>(smem);
-        const uint32_t row_acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * (part / 2);
+        const uint32_t row_acc = quarter + buf * C::BN + half * (part / 2);
         auto sums_at = [&](int sender, int b) {
           return sums + (((sender * C::EPI_WARPS + (warp - 4)) * blocks + b) * 16 * 32) + lane * 4;
         };
@@ -532,7 +574,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         }
         break;  // a cluster has one tile
       }
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * C::BN + half * wide;
+      const uint32_t acc = quarter + buf * C::BN + half * wide;
       // The whole accumulator is read and rounded before anything is stored, so
       // that the MMAs of the tile after next can start (box by box: 32 groups
       // of 512 rows 536 us, so 498).
@@ -555,7 +597,6 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(tempty0 + 8u * buf);
-        ++j;
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -601,7 +642,8 @@ cudaError_t launch_wgrad(const CUtensorMap& ty, const CUtensorMap& tx, const CUt
   const long long tiles = (long long)p.E * ((p.N + kWM - 1) / kWM) * ((p.K + kWN - 1) / kWN);
   const int stages = (int)((p.P / p.E + 63) / 64);
   p.split = 1;
-  // (into fp32 a share of a group of average length is one segment, see kSegment)
+  // (into fp32 a share of a group of average length is one segment, see kSegment: longer ones add up faster in
+  // registers)
   const int most = p.out_type == MOE_DT_FP32 ? 4 * kSegment : 1 << 20;
   while (p.split < 4 && stages <= most && tiles <= resident_clusters(p.split * 4, sms) && stages >= p.split * 2 * kMinStages)
     p.split *= 2;

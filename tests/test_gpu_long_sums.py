@@ -64,3 +64,46 @@ def test_long_products(dtype, counts, M):
     del w
     check(moe.grouped_gemm_dgrad(x, wt, off, status=status), ref)
     assert int(status) == 0
+
+
+@TYPES
+@pytest.mark.parametrize("counts,N,K", [([262149, 8192, 8193, 0, 16385, 3, 32768, 40000] + [0, 70] * 16, 256, 256),
+                                        ([16384, 8191, 24577] * 20, 136, 200), ([1 << 19], 200, 256), ([1 << 18, 5], 40, 72)],
+                         ids=["whole_tiles", "several_tiles_a_pair", "shared_by_four", "shared_by_two_groups"])
+def test_weight_gradients_of_long_groups(dtype, counts, N, K):
+    off = offsets_of(counts)
+    P = sum(counts)
+    gen = torch.Generator("cuda").manual_seed(N)
+    x = positive(gen, P, K, dtype=dtype)
+    dy = positive(gen, P, N, dtype=dtype, scale=2.0 ** -8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dw = moe.grouped_gemm_wgrad(dy, x, off, status=status)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        if a == b:
+            assert not dw[e].any()
+        else:
+            check(dw[e], dy[a:b].double().T @ x[a:b].double())
+    assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off)) and int(status) == 0
+
+
+# The 2-norm that the kernels' comments state for fp32 results of terms of random signs, 1.0e-6 (bf16) and 1.3e-6 (fp16),
+# with half as much again: whatever the length, since the segments' own additions round by 2^-24 (6e-8) each.  One
+# accumulator over 7168 elements is off by 6.6e-6, a result rounded to fp16 by 2e-4.
+NORM = 2e-6
+
+
+@TYPES
+@pytest.mark.parametrize("counts,N,K", [([32768] + [0] * 7, 256, 256), ([0, 20001, 3, 11000, 0, 70], 200, 136)],
+                         ids=["all_in_one", "uneven"])
+def test_shared_weight_gradients_into_fp32_of_uneven_groups(dtype, counts, N, K):
+    """How many pairs share a tile's rows goes by the average group; the accuracy of a longer one may not."""
+    off = offsets_of(counts)
+    P = sum(counts)
+    gen = torch.Generator("cuda").manual_seed(N)
+    dy, x = (torch.randn(P, n, generator=gen, device="cuda").to(dtype) for n in (N, K))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dw = moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32, status=status)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        ref = dy[a:b].double().T @ x[a:b].double()
+        assert float((dw[e].double() - ref).norm()) <= NORM * float(ref.norm()), e
+    assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)) and int(status) == 0
