@@ -20,6 +20,7 @@ import pytest
 import torch
 
 from fp4_block_scaled_route_b200 import moe
+from tests.test_gpu_grouped import WAYS
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,33 @@ def test_shared_weight_gradients_into_fp32_of_uneven_groups(dtype, counts, N, K)
         ref = dy[a:b].double().T @ x[a:b].double()
         assert float((dw[e].double() - ref).norm()) <= NORM * float(ref.norm()), e
     assert torch.equal(dw, moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)) and int(status) == 0
+
+
+def norms_fit(got, ref):
+    assert float((got.double() - ref).norm()) <= NORM * float(ref.norm())
+
+
+@TYPES
+@pytest.mark.parametrize("counts,N,K", [*WAYS.values(), ([3, 0, 9], 1032, 7176), ([60], 1032, 7176), ([700, 40, 300], 1032, 7176),
+                                        ([130, 257, 500, 0, 64] * 3, 1032, 7176)],
+                         ids=[*WAYS, "few_7176", "some_7176", "few_large_7176", "pairs_7176"])
+def test_products_into_fp32_in_the_2_norm(dtype, counts, N, K):
+    """Elementwise bounds have to allow for every addition's worst case; the 2-norm shows what the additions do."""
+    off = offsets_of(counts)
+    gen = torch.Generator("cuda").manual_seed(N + K)
+    x, w = (torch.randn(*s, generator=gen, device="cuda").to(dtype) for s in ((sum(counts), K), (len(counts), N, K)))
+    ref = torch.cat([x[a:b].double() @ w[e].double().T for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))])
+    norms_fit(moe.grouped_gemm(x, w, off, out_dtype=FP32), ref)
+    norms_fit(moe.grouped_gemm_dgrad(x, w.transpose(1, 2).contiguous(), off, out_dtype=FP32), ref)
+
+
+@TYPES
+@pytest.mark.parametrize("counts,N,K", [([5000, 1, 1030, 0, 2048, 1024], 264, 1160), ([9001], 1800, 2056), ([4096], 136, 200),
+                                        ([20000] * 3, 520, 2056), ([300, 7, 0, 900] * 20, 136, 264)])
+def test_weight_gradients_into_fp32_in_the_2_norm(dtype, counts, N, K):
+    off = offsets_of(counts)
+    gen = torch.Generator("cuda").manual_seed(N + K)
+    dy, x = (torch.randn(sum(counts), n, generator=gen, device="cuda").to(dtype) for n in (N, K))
+    dw = moe.grouped_gemm_wgrad(dy, x, off, out_dtype=FP32)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        norms_fit(dw[e], dy[a:b].double().T @ x[a:b].double())
