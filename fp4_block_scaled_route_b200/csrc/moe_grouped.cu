@@ -88,6 +88,9 @@ constexpr int kFewChunks = 24;
 // before it is through loading the present one.
 constexpr int kHandOutChunks = 32;
 constexpr int kAhead = 12;
+// Up to this many: a pair that looks for a unit may meet all the clusters past
+// the last one (0.3 to 1 us each), while its other warps wait within their limit.
+constexpr long long kMaxHandOut = 1LL << 18;
 
 struct Tile {
   int e, m0, p0, rows;
@@ -119,7 +122,7 @@ struct Units {
 };
 
 // Unit u -> group, first feature, first row, rows (none for a piece past the
-// group's end).  e walks upwards with u, which only grows.
+// group's end).  e walks upwards with u, and starts again where u falls.
 template <int BN, int BM>
 __device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off, const int* s_tile, int& e) {
   const int NT = w.NT;
@@ -131,6 +134,7 @@ __device__ __forceinline__ Tile tile_of(int u, const Units& w, const int* s_off,
     u = w.whole + (i >> cut);
   }
   const int v = u / NT;
+  if (s_tile[e] > v) e = 0;
   while (s_tile[e + 1] <= v) ++e;
   const int local = u - s_tile[e] * NT, mt = s_tile[e + 1] - s_tile[e];
   const int band = local / (kBand * NT), in_band = local - band * kBand * NT;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
   const uint32_t taken0 = CG == 2 ? mapa_rank(taken, 0) : 0;
   int hand = 0;
   auto next_unit = [&](int u) {
-    if (!hand_out) return u + teams;
+    if (CG != 2 || !hand_out) return u + teams;
     const int b = hand & 1;
     const bool in = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&handed[b], (uint32_t)(hand >> 1) & 1u, abort));
     const int v = in ? unit[b] : work.total;
@@ -246,6 +250,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     ++hand;
     return v;
   };
+  // The first one: a cluster past the last unit may still be handed some.
+  auto first_unit = [&]() { return CG == 2 && hand_out && team >= work.total ? next_unit(team) : team; };
 
   if (warp == 0) {
     const uint64_t pol_w = p.stream_w ? policy_evict_first() : policy_evict_normal();
@@ -254,7 +260,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     uint32_t armed = 0, st = 0, ph = 0;
     bool ok = true;
     int e = 0;
-    for (int u = team; u < work.total && ok; u = next_unit(u)) {
+    if (hand_out && rank == 0 && lane == 0 && team >= work.total) mbar_arrive(want);
+    for (int u = first_unit(); u < work.total && ok; u = next_unit(u)) {
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       if (t.rows <= 0) {
         if (hand_out && rank == 0 && lane == 0) mbar_arrive(want);
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
       constexpr uint64_t step_a = KIND == GG_DGRAD ? 128 : 2, step_b = 2;
       bool ok = true;
       uint32_t st = 0, ph = 0;
-      int j = 0, e = 0, u = team;
+      int j = 0, e = 0, u = first_unit();
       Tile next = {};
       if (u < work.total) next = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       while (u < work.total && ok) {
@@ -388,13 +395,14 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         *v = block >= 0 ? block / 2 : work.total;
         return block >= 0;
       };
-      for (int i = 0; team < work.total; ++i) {
+      for (int i = 0;; ++i) {
         const int b = i & 1;
         if (!mbar_wait_warp(want, (uint32_t)i & 1u, abort) ||
             !mbar_wait_warp(&taken[b], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort))
           break;
-        int v = work.total;
-        if (left) left = ask(&v);
+        // (the clusters past the last unit are taken off the grid as well, so that they need not start, set up and
+        // leave: offsets that cover few of the rows, or none, leave many)
+        const int v = next_handed(ask, work.total, left);
         if (lane == 0) {
           unit[b] = v;
           asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(unit1 + 4u * b), "r"(v) : "memory");
@@ -404,9 +412,6 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         __syncwarp();
         if (v >= work.total) break;
       }
-      // the clusters past the last unit need not start at all (each would set
-      // up and leave: offsets that cover few of the rows, or none, leave many)
-      for (int v; left;) left = ask(&v);
       // (an answer still on its way lands before the CTA leaves)
       if (*abort && asked) mbar_drain(answered, (uint32_t)(asked - 1) & 1u);
     }
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
     const uint32_t turn_st = smem_u32(turn) + (lane & 7) * 80 + (lane >> 3) * 16;
     bool ok = true;
     int j = 0, e = 0;
-    for (int u = team; u < work.total && ok; u = next_unit(u)) {
+    for (int u = first_unit(); u < work.total && ok; u = next_unit(u)) {
       const Tile t = tile_of<BN, 128 * CG>(u, work, s_off, s_tile, e);
       if (t.rows <= 0) continue;
       const int m0 = t.m0 + (CG == 2 ? (int)rank * 128 : 0) + q * 32;  // this warp's first feature
@@ -654,7 +659,7 @@ GroupedTile grouped_tile(const GroupedParams& p, int kind, int sms) {
     t.grid = t.running = sms / 2 * 2;
     // a cluster for every unit there can be: tiles, and the pieces of the last wave
     const long long units = most(256, 256) + sms / 2;
-    if (p.E > 1 && chunks >= kHandOutChunks && units * 2 < (1LL << 30)) t.grid = (int)units * 2;
+    if (p.E > 1 && chunks >= kHandOutChunks && units <= kMaxHandOut) t.grid = (int)units * 2;
     return t;
   }
   // Shared tiles hold the group's rows when there is one group, else twice the

@@ -344,6 +344,20 @@ __device__ __forceinline__ int cancelled_block(const void* answer) {
   return got ? (int)x : -1;
 }
 
+// The next unit of work below `total`, or `total` when the grid has none left.
+// ask(&v) takes one cluster off the grid (v: its unit), or returns false: none
+// was left, and nothing may be asked again.  Clusters come in no promised
+// order: those past the last unit are passed over, not taken for the end.
+template <typename Ask>
+__device__ __forceinline__ int next_handed(Ask&& ask, int total, bool& left) {
+  while (left) {
+    int v = total;
+    left = ask(&v);
+    if (left && v < total) return v;
+  }
+  return total;
+}
+
 // ---- groups --------------------------------------------------------------------
 // Builds in shared memory the groups' offsets and the first row tile of each
 // group (tiles of `tile_rows` rows).  All THREADS threads of the CTA call it;
