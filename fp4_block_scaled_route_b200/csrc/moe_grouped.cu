@@ -483,10 +483,9 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
         for (int i = 0; i < STEPS * C::CB; ++i) {
           const int c = (i / C::CB * 2 + half) * C::CB + i % C::CB;
           const float v = s[i / C::CB][i % C::CB];
-          if (c >= t.rows || m0 + lane >= p.M) continue;
-          if (p.out_type == MOE_DT_FP32)
-            static_cast<float*>(p.y)[at + (size_t)c * p.ldy] = v;
-          else
+          if (p.out_type == MOE_DT_FP32) {
+            if (c < t.rows && m0 + lane < p.M) static_cast<float*>(p.y)[at + (size_t)c * p.ldy] = v;
+          } else if (c < t.rows && m0 + lane < p.M)
             static_cast<uint16_t*>(p.y)[at + (size_t)c * p.ldy] = (uint16_t)pack16(v, 0.0f, p.out_type == MOE_DT_BF16);
         }
         __syncwarp();
@@ -580,8 +579,8 @@ __global__ void __launch_bounds__(Cfg<KIND, BN, CG, SPLIT>::THREADS, 1)
             if (p.out_type == MOE_DT_FP32) continue;
             stmatrix_x4_trans(turn_st + i * 8 * 80, w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();  // the next step's accumulators are read by the whole warp
           if (p.out_type == MOE_DT_FP32) continue;
-          __syncwarp();
           uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(t.p0 + c0) * p.ldy + m0;
 #pragma unroll
           for (int i = 0; i < C::CB / 8; ++i) {

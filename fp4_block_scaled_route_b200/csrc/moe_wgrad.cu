@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_at(mapa_rank(joined, 2 * pr + rank));
+          __syncwarp();
         }
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(joined, 0, abort));
         if (!ok) break;
@@ -556,21 +557,22 @@ __global__ void __launch_bounds__(WCfg<STAGES>::THREADS, 1)
           const int k = t.k0 + pair * part + half * (part / 2) + b * 16;
           const size_t at = ((size_t)t.e * p.N + n + lane) * p.K + k;
           // (K is a multiple of 16 bytes: no piece is partly inside)
-          if (n + lane >= p.N) continue;
+          const int cols = n + lane < p.N ? p.K - k : 0;
           if (f32) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              if (k + i < p.K)
+              if (i < cols)
                 *reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at + i) =
                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; i += 8)
-              if (k + i < p.K)
+              if (i < cols)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw) + at + i) =
                     make_uint4(pack16(v[i], v[i + 1], bf), pack16(v[i + 2], v[i + 3], bf),
                                pack16(v[i + 4], v[i + 5], bf), pack16(v[i + 6], v[i + 7], bf));
           }
+          __syncwarp();  // the next block's accumulators are read by the whole warp
         }
         break;  // a cluster has one tile
       }
