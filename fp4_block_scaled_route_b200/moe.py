@@ -518,6 +518,11 @@ def _matrix(t, rows, cols, what, name):
     return -(-shape[1] // step) * step
 
 
+def _given(t, what, name):
+    if t is None:
+        raise ValueError(f"{what}: {name} is None")
+
+
 def _vector(t, n, what, name):
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
@@ -540,6 +545,7 @@ def _weights(w, offsets, what):
 
 def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, status, stream):
     import torch
+    _given(offsets, what, "offsets")
     E, N, K, ldw, sw = _weights(w, offsets, what)
     P = rows.shape[0]
     R, M = (K, N) if forward else (N, K)
@@ -590,6 +596,7 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
     what = "grouped_gemm_wgrad"
     lddy = _matrix(dy, None, None, what, "dy")
     ldx = _matrix(x, dy.shape[0], None, what, "x")
+    _given(offsets, what, "offsets")
     (P, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
     _vector(offsets, E + 1, what, "offsets")
     dtype = dy.dtype
@@ -683,6 +690,7 @@ def permute(x, perm, k, out=None, stream=None):
     what = "permute"
     ldx = _matrix(x, None, None, what, "x")
     T, H = x.shape
+    _given(perm, what, "perm")
     rows = perm.shape[0]
     _vector(perm, rows, what, "perm")
     dt = _dtype_code(x.dtype, what)
@@ -701,6 +709,7 @@ def permute(x, perm, k, out=None, stream=None):
 
 def _combine_sizes(inv, topk_w, k, n_shared, what):
     """(T, k) from the slots' count; topk_w [T, k], or None with k given."""
+    _given(inv, what, "inv")
     if topk_w is not None:
         if topk_w.dim() != 2 or (k is not None and topk_w.shape[1] != k):
             raise ValueError(f"{what}: topk_w has shape {tuple(topk_w.shape)}, not [T, k]")
@@ -742,6 +751,7 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     left as they were (unspecified in a `dy` made here)."""
     import torch
     what = "combine_backward"
+    _given(topk_w, what, "topk_w")
     T, k = _combine_sizes(inv, topk_w, None, n_shared, what)
     ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
