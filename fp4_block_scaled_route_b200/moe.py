@@ -518,6 +518,15 @@ def _matrix(t, rows, cols, what, name):
     return -(-shape[1] // step) * step
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fits(what, *sizes):
+    """Refuses what the library does not take, where ctypes would pass the low 32 bits of it."""
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX:
+        raise MoeError(MOE_ERR_UNSUPPORTED, what)
+
+
 def _given(t, what, name):
     if t is None:
         raise ValueError(f"{what}: {name} is None")
@@ -548,6 +557,7 @@ def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, statu
     _given(offsets, what, "offsets")
     E, N, K, ldw, sw = _weights(w, offsets, what)
     P = rows.shape[0]
+    _fits(what, E, P, N, K)
     R, M = (K, N) if forward else (N, K)
     ld = _matrix(rows, P, R, what, name)
     dtype = rows.dtype
@@ -598,6 +608,7 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
     ldx = _matrix(x, dy.shape[0], None, what, "x")
     _given(offsets, what, "offsets")
     (P, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
+    _fits(what, E, P, N, K)
     _vector(offsets, E + 1, what, "offsets")
     dtype = dy.dtype
     out_dtype = out.dtype if out is not None else (out_dtype or dtype)
@@ -627,6 +638,7 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
     ldx = _matrix(x, None, None, what, "x")
     T, K = x.shape
     rows = T if perm is None else perm.shape[0]
+    _fits(what, T, K, rows, k)
     dt = _dtype_code(x.dtype, what)
     dev = x.get_device()
     _on(what, max(dev, 0), "x", x, x.dtype)
@@ -661,6 +673,7 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
     else:
         E, N, K, ldw, sw = _weights(w, offsets, what)
     P = q.shape[0]
+    _fits(what, E, P, N, K)
     ldq = _matrix(q, P, K, what, "q")
     _vector(q_scale, P, what, "q_scale")
     _vector(w_scale, E * N, what, "w_scale")
@@ -692,6 +705,7 @@ def permute(x, perm, k, out=None, stream=None):
     T, H = x.shape
     _given(perm, what, "perm")
     rows = perm.shape[0]
+    _fits(what, T, H, rows, k)
     _vector(perm, rows, what, "perm")
     dt = _dtype_code(x.dtype, what)
     dev = x.get_device()
@@ -731,6 +745,7 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
     ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
     T, k = _combine_sizes(inv, topk_w, k, n_shared, what)
+    _fits(what, rows, H, T, k, n_shared)
     dt = _dtype_code(y.dtype, what)
     dev = y.get_device()
     _on(what, max(dev, 0), "y", y, y.dtype)
@@ -755,6 +770,7 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     T, k = _combine_sizes(inv, topk_w, None, n_shared, what)
     ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
+    _fits(what, rows, H, T, k, n_shared)
     ldd = _matrix(dout, T, H, what, "dout")
     dt = _dtype_code(y.dtype, what)
     dev = y.get_device()

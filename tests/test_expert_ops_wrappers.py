@@ -27,3 +27,39 @@ W, OFF, PERM = torch.zeros(2, 16, 32), torch.zeros(3, dtype=torch.int32), torch.
 def test_a_missing_argument_is_named(call, name):
     with pytest.raises(ValueError, match=f"{name} is None"):
         call()
+
+
+BIG = 2 ** 32 + 4    # its low 32 bits are 4
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def index(n):
+    return meta(n, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: moe.grouped_gemm(meta(BIG, 32), meta(2, 16, 32), index(3)),
+    lambda: moe.grouped_gemm(meta(4, 32), meta(2, BIG, 32), index(3)),
+    lambda: moe.grouped_gemm_dgrad(meta(BIG, 16), meta(2, 16, 32), index(3)),
+    lambda: moe.grouped_gemm_wgrad(meta(BIG, 16), meta(BIG, 32), index(3)),
+    lambda: moe.grouped_gemm_wgrad(meta(4, 16), meta(4, 32), index(BIG)),
+    lambda: moe.quant_int8(meta(BIG, 32)),
+    lambda: moe.quant_int8(meta(4, 32), perm=index(BIG), k=2),
+    lambda: moe.quant_int8(meta(4, 32), perm=index(8), k=2 ** 32 + 2),
+    lambda: moe.int8_gemm(meta(BIG, 32, dtype=torch.int8), meta(BIG), meta(16, 32, dtype=torch.int8), meta(16)),
+    lambda: moe.permute(meta(BIG, 32), index(8), 2),
+    lambda: moe.permute(meta(4, 32), index(BIG), 2),
+    lambda: moe.permute(meta(4, 32), index(8), 2 - 2 ** 32),
+    lambda: moe.combine(meta(BIG, 32), index(8), k=2),
+    lambda: moe.combine(meta(8, 32), index(2 * BIG), k=2),
+    lambda: moe.combine(meta(8, 32), index(0), k=2 ** 32 + 2),
+    lambda: moe.combine_backward(meta(BIG, 32), meta(8, 32), index(2 * BIG), meta(BIG, 2)),
+])
+def test_sizes_past_32_bits_are_refused(call):
+    """ctypes passes the low 32 bits of a size: such a call would work on the first few rows without a word."""
+    with pytest.raises(moe.MoeError) as e:
+        call()
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED
