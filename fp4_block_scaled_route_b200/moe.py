@@ -732,6 +732,8 @@ def _combine_sizes(inv, topk_w, k, n_shared, what):
     else:
         if k is None:
             raise ValueError(f"{what}: without topk_w, k has to be given")
+        if k < 1 or n_shared < 0:
+            raise ValueError(f"{what}: k is {k}, n_shared is {n_shared}")
         T = inv.numel() // (k + n_shared)
     _vector(inv, T * (k + n_shared), what, "inv")
     return T, k

@@ -63,3 +63,10 @@ def test_sizes_past_32_bits_are_refused(call):
     with pytest.raises(moe.MoeError) as e:
         call()
     assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("k,n_shared", [(0, 0), (0, 1), (-1, 1), (2, -2), (2, -1)])
+def test_slots_that_no_token_has_are_refused(k, n_shared):
+    """The number of tokens is that of the slots by k + n_shared."""
+    with pytest.raises(ValueError, match="k is"):
+        moe.combine(rows(), PERM, k=k, n_shared=n_shared)
