@@ -443,6 +443,12 @@ void moe_destroy(moe_ctx* c) {
   delete c;
 }
 
+// A launch goes to the current device, the workspace lies on the context's.
+static bool on_device(const moe_ctx* c) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == c->dev;
+}
+
 // The launch sequence of one layer for every weight format; g13 / g2 are the
 // NVFP4 global scales (null for the other formats).  With partial_out the
 // fp32 combine result goes to that caller buffer (GEMM2 reduces into it) and
@@ -450,7 +456,7 @@ void moe_destroy(moe_ctx* c) {
 static moe_status forward_impl(moe_ctx* c, int T, const void* x, const int32_t* ids, const float* topk_w,
                                const void* w13, const void* s13, const float* g13, const void* w2, const void* s2,
                                const float* g2, void* out, void* stream, float* partial_out = nullptr) {
-  if (!c || T < 0 || T > c->max_T) return MOE_ERR_INVALID_ARG;
+  if (!c || T < 0 || T > c->max_T || !on_device(c)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const bool partial = partial_out != nullptr;
   if (!x || !ids || !topk_w || !w13 || !s13 || !w2 || !s2 || (!out && !partial)) return MOE_ERR_INVALID_ARG;
@@ -708,7 +714,7 @@ moe_status moe_forward_nvfp4(moe_ctx* c, int T, const void* x, const int32_t* id
 
 moe_status moe_router_topk(moe_ctx* c, int T, const void* x, const void* wr, int32_t* topk_ids, float* topk_w,
                            void* stream) {
-  if (!c || T < 0 || T > c->max_T) return MOE_ERR_INVALID_ARG;
+  if (!c || T < 0 || T > c->max_T || !on_device(c)) return MOE_ERR_INVALID_ARG;
   if (!c->rt_logits) return MOE_ERR_UNSUPPORTED;  // E > 256 or E % 4 != 0
   if (T == 0) return MOE_OK;
   if (!x || !wr || !topk_ids || !topk_w || !aligned(x, 16) || !aligned(wr, 16) || !aligned(topk_ids, 4) ||
@@ -984,7 +990,8 @@ moe_status moe_set_fault_injection(moe_ctx* c, int mode) {
 
 moe_status moe_route(moe_ctx* c, int T, const int32_t* ids, int32_t* counts, int32_t* offsets, int32_t* perm,
                      int32_t* inv, void* stream) {
-  if (!c || T < 0 || T > c->max_T || !counts || !offsets || !aligned(counts, 4) || !aligned(offsets, 4))
+  if (!c || T < 0 || T > c->max_T || !counts || !offsets || !aligned(counts, 4) || !aligned(offsets, 4) ||
+      !on_device(c))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0)

@@ -288,6 +288,8 @@ class MoeLayer:
         self.H, self.I, self.E, self.k, self.wfmt = H, I, E, k, wfmt
         self.max_T, self.n_shared = max_T, n_shared
         self.ctx = moe_create_ex(H, I, E, k, wfmt, max_T, n_shared)
+        import torch
+        self.device = torch.cuda.current_device()   # the context's
 
     def close(self):
         if self.ctx:
@@ -402,8 +404,8 @@ class MoeLayer:
             raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, {self.k}]")
         NG, P = self.E + self.n_shared, T * (self.k + self.n_shared)
         _vector(topk_ids, P - T * self.n_shared, "route", "topk_ids")
-        dev = topk_ids.get_device()
-        _on("route", max(dev, 0), "topk_ids", topk_ids, torch.int32)
+        dev = self.device
+        _on("route", dev, "topk_ids", topk_ids, torch.int32)
 
         def body(s):
             counts, offsets, perm, inv = (torch.empty(n, dtype=torch.int32, device=dev) for n in (NG, NG + 1, P, P))

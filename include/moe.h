@@ -25,6 +25,8 @@
  * Conventions for every entry point:
  *   - Pointers named d_* or documented as "device" are CUDA device pointers on
  *     the context's device; the library never frees memory it did not allocate.
+ *   - The device that was current at moe_create() is current at every call that
+ *     computes on the context; another one is MOE_ERR_INVALID_ARG.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  All work is
  *     enqueued asynchronously on it; no entry point synchronises the device
  *     unless documented.

@@ -70,3 +70,30 @@ def test_slots_that_no_token_has_are_refused(k, n_shared):
     """The number of tokens is that of the slots by k + n_shared."""
     with pytest.raises(ValueError, match="k is"):
         moe.combine(rows(), PERM, k=k, n_shared=n_shared)
+
+
+class OnAnotherGpu:
+    """Ids [2, 2] as route() sees a tensor of cuda:1."""
+    shape, device, dtype, is_cuda = torch.Size((2, 2)), torch.device("cuda", 1), torch.int32, True
+
+    def numel(self):
+        return 4
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        raise AssertionError("reached the library")
+
+
+def test_route_refuses_ids_of_another_gpu():
+    """The context's workspace lies on its own GPU."""
+    layer = object.__new__(moe.MoeLayer)
+    layer.E, layer.k, layer.n_shared, layer.device, layer.ctx = 4, 2, 0, 0, None
+    with pytest.raises(ValueError, match="topk_ids is on cuda:1, not on cuda:0"):
+        layer.route(OnAnotherGpu())
+    with pytest.raises(ValueError, match="not a CUDA tensor"):
+        layer.route(torch.zeros(2, 2, dtype=torch.int32))
