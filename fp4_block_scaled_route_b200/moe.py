@@ -483,6 +483,41 @@ def _call(what, dev, stream, body):
         return body(torch._C._cuda_getCurrentRawStream(dev))
 
 
+_no_formula = None
+
+
+def _results(what, made, given, *inputs):
+    """`made`, the result of a call, as autograd has to see it.
+
+    These operators have no autograd formula: their gradients are calls of their own.  If an input records a gradient, a
+    backward pass through what is returned raises.  A caller's tensor that the result was written into (`given`) has a
+    new version, so that a graph which kept its old values notices."""
+    if given is not None:
+        from torch.autograd.graph import increment_version
+        increment_version(given)
+    for t in inputs:
+        if t.requires_grad:
+            break
+    else:
+        return made
+    import torch
+    if not torch.is_grad_enabled():
+        return made
+    global _no_formula
+    if _no_formula is None:
+        class NoFormula(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, what, made, *inputs):
+                ctx.what = what
+                return made   # (another tensor of the same memory: a caller's own stays outside of the graph)
+
+            @staticmethod
+            def backward(ctx, *grads):
+                raise NotImplementedError(f"moe.{ctx.what} has no autograd formula: its gradient is a call of its own")
+        _no_formula = NoFormula
+    return _no_formula.apply(what, made, *inputs)
+
+
 def _dtype_code(dtype, what):
     import torch
     if dtype is torch.bfloat16:
@@ -523,15 +558,13 @@ def _matrix(t, rows, cols, what, name):
 _INT_MAX = 2 ** 31 - 1
 
 
-def _fits(what, *sizes):
-    """Refuses what the library does not take, where ctypes would pass the low 32 bits of it."""
-    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX:
-        raise MoeError(MOE_ERR_UNSUPPORTED, what)
+def _too_large(what):
+    """What the library does not take, and ctypes would pass the low 32 bits of."""
+    raise MoeError(MOE_ERR_UNSUPPORTED, what)
 
 
-def _given(t, what, name):
-    if t is None:
-        raise ValueError(f"{what}: {name} is None")
+def _missing(what, name):
+    raise ValueError(f"{what}: {name} is None")
 
 
 def _vector(t, n, what, name):
@@ -556,10 +589,12 @@ def _weights(w, offsets, what):
 
 def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, status, stream):
     import torch
-    _given(offsets, what, "offsets")
+    if offsets is None:
+        _missing(what, "offsets")
     E, N, K, ldw, sw = _weights(w, offsets, what)
     P = rows.shape[0]
-    _fits(what, E, P, N, K)
+    if E + P + N + K > _INT_MAX:
+        _too_large(what)
     R, M = (K, N) if forward else (N, K)
     ld = _matrix(rows, P, R, what, name)
     dtype = rows.dtype
@@ -583,7 +618,10 @@ def _grouped(entry, what, name, rows, forward, w, offsets, out, out_dtype, statu
         if st != MOE_OK:
             raise MoeError(st, entry)
         return y
-    return _call(what, dev, stream, body)
+    y = _call(what, dev, stream, body)
+    if out is None and not (rows.requires_grad or w.requires_grad):
+        return y
+    return _results(what, y, out, rows, w)
 
 
 def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=None):
@@ -608,9 +646,11 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
     what = "grouped_gemm_wgrad"
     lddy = _matrix(dy, None, None, what, "dy")
     ldx = _matrix(x, dy.shape[0], None, what, "x")
-    _given(offsets, what, "offsets")
+    if offsets is None:
+        _missing(what, "offsets")
     (P, N), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
-    _fits(what, E, P, N, K)
+    if E + P + N + K > _INT_MAX:
+        _too_large(what)
     _vector(offsets, E + 1, what, "offsets")
     dtype = dy.dtype
     out_dtype = out.dtype if out is not None else (out_dtype or dtype)
@@ -629,7 +669,7 @@ def grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, status=None, st
         _check(lib().moe_grouped_gemm_wgrad(dt, odt, E, P, N, K, offsets.data_ptr(), dy.data_ptr(), lddy, x.data_ptr(),
                                             ldx, dw.data_ptr(), _ptr(status), s), "moe_grouped_gemm_wgrad")
         return dw
-    return _call(what, dev, stream, body)
+    return _results(what, _call(what, dev, stream, body), out, dy, x)
 
 
 def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
@@ -640,7 +680,8 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
     ldx = _matrix(x, None, None, what, "x")
     T, K = x.shape
     rows = T if perm is None else perm.shape[0]
-    _fits(what, T, K, rows, k)
+    if T + K + rows + abs(k) > _INT_MAX:
+        _too_large(what)
     dt = _dtype_code(x.dtype, what)
     dev = x.get_device()
     _on(what, max(dev, 0), "x", x, x.dtype)
@@ -657,7 +698,10 @@ def quant_int8(x, perm=None, k=1, out=None, scale=None, stream=None):
         _check(lib().moe_quant_int8(dt, rows, K, T, k, x.data_ptr(), ldx, _ptr(perm), q.data_ptr(), ldq,
                                     sc.data_ptr(), s), "moe_quant_int8")
         return q, sc
-    return _call(what, dev, stream, body)
+    q, sc = _call(what, dev, stream, body)
+    if out is None and scale is None and not x.requires_grad:
+        return q, sc
+    return _results(what, q, out), _results(what, sc, scale, x)
 
 
 def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, status=None, stream=None):
@@ -675,7 +719,8 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
     else:
         E, N, K, ldw, sw = _weights(w, offsets, what)
     P = q.shape[0]
-    _fits(what, E, P, N, K)
+    if E + P + N + K > _INT_MAX:
+        _too_large(what)
     ldq = _matrix(q, P, K, what, "q")
     _vector(q_scale, P, what, "q_scale")
     _vector(w_scale, E * N, what, "w_scale")
@@ -695,7 +740,10 @@ def int8_gemm(q, q_scale, w, w_scale, offsets=None, out=None, out_dtype=None, st
         _check(lib().moe_int8_gemm(odt, E, P, N, K, _ptr(offsets), q.data_ptr(), ldq, q_scale.data_ptr(), w.data_ptr(),
                                    ldw, sw, w_scale.data_ptr(), y.data_ptr(), ldy, _ptr(status), s), "moe_int8_gemm")
         return y
-    return _call(what, dev, stream, body)
+    y = _call(what, dev, stream, body)
+    if out is None and not (q_scale.requires_grad or w_scale.requires_grad):
+        return y
+    return _results(what, y, out, q_scale, w_scale)
 
 
 def permute(x, perm, k, out=None, stream=None):
@@ -705,9 +753,11 @@ def permute(x, perm, k, out=None, stream=None):
     what = "permute"
     ldx = _matrix(x, None, None, what, "x")
     T, H = x.shape
-    _given(perm, what, "perm")
+    if perm is None:
+        _missing(what, "perm")
     rows = perm.shape[0]
-    _fits(what, T, H, rows, k)
+    if T + H + rows + abs(k) > _INT_MAX:
+        _too_large(what)
     _vector(perm, rows, what, "perm")
     dt = _dtype_code(x.dtype, what)
     dev = x.get_device()
@@ -720,12 +770,16 @@ def permute(x, perm, k, out=None, stream=None):
         _check(lib().moe_permute(dt, rows, H, T, k, x.data_ptr(), ldx, perm.data_ptr(), y.data_ptr(), ldy, s),
                "moe_permute")
         return y
-    return _call(what, dev, stream, body)
+    y = _call(what, dev, stream, body)
+    if out is None and not x.requires_grad:
+        return y
+    return _results(what, y, out, x)
 
 
 def _combine_sizes(inv, topk_w, k, n_shared, what):
     """(T, k) from the slots' count; topk_w [T, k], or None with k given."""
-    _given(inv, what, "inv")
+    if inv is None:
+        _missing(what, "inv")
     if topk_w is not None:
         if topk_w.dim() != 2 or (k is not None and topk_w.shape[1] != k):
             raise ValueError(f"{what}: topk_w has shape {tuple(topk_w.shape)}, not [T, k]")
@@ -749,7 +803,8 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
     ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
     T, k = _combine_sizes(inv, topk_w, k, n_shared, what)
-    _fits(what, rows, H, T, k, n_shared)
+    if rows + H + T + k + n_shared > _INT_MAX:
+        _too_large(what)
     dt = _dtype_code(y.dtype, what)
     dev = y.get_device()
     _on(what, max(dev, 0), "y", y, y.dtype)
@@ -762,7 +817,11 @@ def combine(y, inv, topk_w=None, k=None, n_shared=0, out=None, stream=None):
         _check(lib().moe_combine(dt, rows, H, T, k, n_shared, y.data_ptr(), ldy, inv.data_ptr(), _ptr(topk_w),
                                  o.data_ptr(), ldo, s), "moe_combine")
         return o
-    return _call(what, dev, stream, body)
+    o = _call(what, dev, stream, body)
+    weights = y if topk_w is None else topk_w
+    if out is None and not (y.requires_grad or weights.requires_grad):
+        return o
+    return _results(what, o, out, y, weights)
 
 
 def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, stream=None):
@@ -770,11 +829,13 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
     left as they were (unspecified in a `dy` made here)."""
     import torch
     what = "combine_backward"
-    _given(topk_w, what, "topk_w")
+    if topk_w is None:
+        _missing(what, "topk_w")
     T, k = _combine_sizes(inv, topk_w, None, n_shared, what)
     ldy = _matrix(y, None, None, what, "y")
     rows, H = y.shape
-    _fits(what, rows, H, T, k, n_shared)
+    if rows + H + T + k + n_shared > _INT_MAX:
+        _too_large(what)
     ldd = _matrix(dout, T, H, what, "dout")
     dt = _dtype_code(y.dtype, what)
     dev = y.get_device()
@@ -793,4 +854,5 @@ def combine_backward(dout, y, inv, topk_w, n_shared=0, dy=None, dtopk_w=None, st
                                           inv.data_ptr(), topk_w.data_ptr(), gy.data_ptr(), lddy, gw.data_ptr(), s),
                "moe_combine_backward")
         return gy, gw
-    return _call(what, dev, stream, body)
+    gy, gw = _call(what, dev, stream, body)
+    return _results(what, gy, dy, dout, topk_w), _results(what, gw, dtopk_w, dout, y)

@@ -97,3 +97,89 @@ def test_route_refuses_ids_of_another_gpu():
         layer.route(OnAnotherGpu())
     with pytest.raises(ValueError, match="not a CUDA tensor"):
         layer.route(torch.zeros(2, 2, dtype=torch.int32))
+
+
+# ---- autograd ---------------------------------------------------------------------
+def z(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+# name -> (call of (inputs, results), shapes of the inputs that may record a gradient, shapes of the results)
+BF16, INT8 = torch.bfloat16, torch.int8
+CALLS = {
+    "grouped_gemm": (lambda i, o: moe.grouped_gemm(i[0], i[1], OFF, out=o[0]), [(4, 32), (2, 16, 32)], [(4, 16)], BF16),
+    "grouped_gemm_dgrad": (lambda i, o: moe.grouped_gemm_dgrad(i[0], i[1], OFF, out=o[0]), [(4, 16), (2, 16, 32)], [(4, 32)], BF16),
+    "grouped_gemm_wgrad": (lambda i, o: moe.grouped_gemm_wgrad(i[0], i[1], OFF, out=o[0]), [(4, 16), (4, 32)], [(2, 16, 32)], BF16),
+    "quant_int8": (lambda i, o: moe.quant_int8(i[0], out=z(4, 32, dtype=INT8), scale=o[0])[1], [(4, 32)], [(4,)], BF16),
+    "int8_gemm": (lambda i, o: moe.int8_gemm(z(4, 32, dtype=INT8), i[0], z(16, 32, dtype=INT8), i[1], out=o[0]), [(4,), (16,)],
+                  [(4, 16)], torch.float32),
+    "permute": (lambda i, o: moe.permute(i[0], PERM, 2, out=o[0]), [(2, 32)], [(4, 32)], BF16),
+    "combine": (lambda i, o: moe.combine(i[0], PERM, i[1], out=o[0]), [(4, 32), (2, 2)], [(2, 32)], torch.float32),
+    "combine_unweighted": (lambda i, o: moe.combine(i[0], PERM, k=2, out=o[0]), [(4, 32)], [(2, 32)], BF16),
+    "combine_backward": (lambda i, o: moe.combine_backward(i[0], i[1], PERM, i[2], dy=o[0], dtopk_w=o[1]),
+                         [(2, 32), (4, 32), (2, 2)], [(4, 32), (2, 2)], torch.float32),
+}
+
+
+class Accepts:
+    """A library that takes every call and computes nothing."""
+    def __getattr__(self, name):
+        return lambda *a: moe.MOE_OK
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    """The wrappers on CPU tensors, up to the library's door."""
+    monkeypatch.setattr(moe, "lib", Accepts)
+    monkeypatch.setattr(moe, "_on", lambda *a: None)
+    monkeypatch.setattr(moe, "_call", lambda what, dev, stream, body: body(0))
+
+
+def tensors(name):
+    _, ins, outs, dtype = CALLS[name]
+    f32 = ("quant_int8",)
+    return [z(*s, dtype=dtype) for s in ins], [z(*s, dtype=torch.float32 if name in f32 else dtype) for s in outs]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_backward_pass_through_a_result_raises(no_library, name):
+    call = CALLS[name][0]
+    for which in range(len(CALLS[name][1])):
+        ins, outs = tensors(name)
+        ins[which].requires_grad_()
+        got = call(ins, outs)
+        got = got if isinstance(got, tuple) else (got,)
+        # dtopk_w does not depend on topk_w, nor dy on y
+        linked = [g for i, g in enumerate(got) if name != "combine_backward" or (i, which) not in ((1, 2), (0, 1))]
+        assert linked and all(g.requires_grad for g in linked)
+        for g, o in zip(got, outs):
+            assert g.data_ptr() == o.data_ptr() and g.stride() == o.stride()
+            assert o.grad_fn is None and not o.requires_grad   # a buffer that is used again gathers no graph
+        for g in linked:
+            with pytest.raises(NotImplementedError, match="no autograd formula"):
+                g.float().sum().backward()
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_without_gradients_stay_outside_of_autograd(no_library, name):
+    call = CALLS[name][0]
+    for grad in (False, True):
+        ins, outs = tensors(name)
+        for i in ins:
+            i.requires_grad_(grad)
+        with torch.set_grad_enabled(not grad):
+            got = call(ins, outs)
+        for g, o in zip(got if isinstance(got, tuple) else (got,), outs):
+            assert g is o and not g.requires_grad and g.grad_fn is None
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_graph_that_kept_an_overwritten_tensor_notices(no_library, name):
+    call = CALLS[name][0]
+    ins, outs = tensors(name)
+    leaves = [torch.ones_like(o, requires_grad=True) for o in outs]
+    kept = [leaf * o for leaf, o in zip(leaves, outs)]     # the product's backward reads o
+    call(ins, outs)
+    for k in kept:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            k.float().sum().backward()
