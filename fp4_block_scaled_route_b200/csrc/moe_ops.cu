@@ -1,14 +1,20 @@
 // moe_ops.cu -- C ABI of the expert operators (include/moe.h): argument
 // checks, tensor maps and launches.  None of them keeps state: no workspace,
-// no allocation, nothing cached between calls.
+// no allocation, nothing cached between calls, but for a word per device that
+// collects the errors of calls without a status word of their own.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "moe.h"
 #include "moe_internal.h"
 #include "moe_ops.h"
+#include "moe_ptx.cuh"
 
 namespace {
+
+__device__ int32_t g_status, g_taken;  // errors since they were last taken; what was taken
+
+__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0); }
 
 using moe::GroupedParams;
 
@@ -81,6 +87,20 @@ moe_status device_sms(int* sms) {
   return MOE_OK;
 }
 
+// Where a call's kernels report: the caller's word, or the current device's.
+moe_status status_word(int32_t** d_status) {
+  static std::atomic<int32_t*> known[64];
+  if (*d_status) return MOE_OK;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev < 64 && (*d_status = known[dev].load(std::memory_order_relaxed)) != nullptr) return MOE_OK;
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return MOE_ERR_CUDA;
+  *d_status = static_cast<int32_t*>(p);
+  if (dev < 64) known[dev].store(*d_status, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
 moe_status sizes_ok(int E, int P, int N, int K) {
   if (E < 1 || P < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || P > kMaxRows || N > kMaxDim || K > kMaxDim) return MOE_ERR_UNSUPPORTED;
@@ -113,6 +133,8 @@ moe_status run_grouped(int kind, int dtype, int out_dtype, int E, int P, int N, 
   int sms = 0;
   const moe_status ds = device_sms(&sms);
   if (ds != MOE_OK) return ds;
+  const moe_status sw = status_word(&d_status);
+  if (sw != MOE_OK) return sw;
   GroupedParams p{};
   p.E = E; p.P = P; p.M = M; p.R = R;
   p.offsets = offsets;
@@ -170,6 +192,8 @@ moe_status moe_grouped_gemm_wgrad(int dtype, int out_dtype, int E, int P, int N,
   const moe_status ds = device_sms(&sms);
   if (ds != MOE_OK) return ds;
   if ((long long)E * ((N + 255) / 256) * ((K + 255) / 256) > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  const moe_status sw = status_word(&d_status);
+  if (sw != MOE_OK) return sw;
   moe::WgradParams p{};
   p.E = E; p.P = P; p.N = N; p.K = K;
   p.offsets = offsets;
@@ -186,6 +210,17 @@ moe_status moe_grouped_gemm_wgrad(int dtype, int out_dtype, int E, int P, int N,
       !make_map(&to, map_type(out_dtype), oes, dw, K, N, K, E, (long long)N * K, 32))
     return MOE_ERR_CUDA;
   return moe::launch_wgrad(ty, tx, to, ty16, tx16, p, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_ops_status(void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  take_status_kernel<<<1, 1, 0, s>>>();
+  int32_t v = 0;
+  if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyFromSymbol(&v, g_taken, sizeof(v)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (v & moe::DEV_TIMEOUT) return MOE_ERR_TIMEOUT;
+  return v & moe::DEV_BAD_ROUTING ? MOE_ERR_BAD_ROUTING : MOE_OK;
 }
 
 moe_status moe_int8_gemm(int out_dtype, int E, int P, int N, int K, const int32_t* offsets, const int8_t* q,

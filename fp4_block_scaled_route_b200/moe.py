@@ -73,6 +73,7 @@ SIGNATURES = {
     "moe_grouped_gemm_wgrad": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp]),
     "moe_quant_int8": (_i, [_i, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _ll, _vp, _vp]),
     "moe_int8_gemm": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _ll, _vp, _vp, _ll, _ll, _vp, _vp, _ll, _vp, _vp]),
+    "moe_ops_status": (_i, [_vp]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -268,6 +269,10 @@ def moe_int8_gemm(out_dtype, E, P, N, K, offsets, q, ldq, q_scale, w, ldw, strid
                   stream) -> int:
     return lib().moe_int8_gemm(out_dtype, E, P, N, K, offsets, q, ldq, q_scale, w, ldw, stride_w, w_scale, y, ldy,
                                d_status, stream)
+
+
+def moe_ops_status(stream) -> int:
+    return lib().moe_ops_status(stream)
 
 
 # ---- torch convenience wrapper (marshalling only) ------------------------
@@ -483,6 +488,15 @@ def _call(what, dev, stream, body):
         return body(torch._C._cuda_getCurrentRawStream(dev))
 
 
+def ops_status(stream=None) -> int:
+    """Errors of the expert operators called without `status` on the stream's device (default: the current one) since the
+    last such question: MOE_OK, MOE_ERR_BAD_ROUTING (unusable offsets: a result made by the call is unset) or
+    MOE_ERR_TIMEOUT (moe_ops_status).  Waits for the stream."""
+    import torch
+    with torch.cuda.stream(stream):
+        return moe_ops_status(_stream_handle(stream))
+
+
 _no_formula = None
 
 
@@ -629,7 +643,8 @@ def grouped_gemm(x, w, offsets, out=None, out_dtype=None, status=None, stream=No
 
     x [P, K] and w [E, N, K] bf16 or fp16 with contiguous rows (any row and expert strides that are multiples of 16
     bytes), offsets device int32 [E+1]; out [P, N] in the same type or fp32.  Rows outside every group are left as
-    they were (unspecified in an `out` made here).  status: optional device int32, see moe.h."""
+    they were (unspecified in an `out` made here).  status: device int32 that errors found on the device are ORed into
+    (see moe.h); without one, ops_status() tells of them."""
     return _grouped("moe_grouped_gemm", "grouped_gemm", "x", x, True, w, offsets, out, out_dtype, status, stream)
 
 

@@ -430,14 +430,23 @@ moe_status moe_forward_noalloc(int H, int I, int E, int k, int wfmt, int n_share
  *     writes them).  A group may be empty.  Output rows outside every group
  *     are left as they were.  Offsets that fall, are negative or pass P are
  *     found on the device: nothing is computed.
- *   - d_status: optional device int32, cleared by the caller, into which the
- *     kernel ORs 1 (unusable offsets) or 2 (a pipeline wait gave up).
+ *   - d_status: device int32, cleared by the caller, into which the kernel ORs
+ *     1 (unusable offsets) or 2 (a pipeline wait gave up; outputs invalid).
+ *     NULL: these errors go to the current device's word, which
+ *     moe_ops_status() reads.
  *   - Sizes past P <= 2^24 rows or N, K <= 2^20: MOE_ERR_UNSUPPORTED.
  *   - Sums are held in fp32 (int8 products: exact int32) and rounded once,
  *     to nearest even, to the output type. */
 
 /* Element types. */
 enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 };
+
+/* moe_ops_status -- errors of calls of this section made with d_status NULL on
+ * the current device, from any stream, since the last such question.
+ * Synchronises `stream` (so it cannot be captured) and returns MOE_OK,
+ * MOE_ERR_BAD_ROUTING (unusable offsets: nothing was computed) or
+ * MOE_ERR_TIMEOUT (a pipeline wait gave up), and clears the word. */
+moe_status moe_ops_status(void* stream);
 
 /* moe_route -- the routing arrays of topk_ids (device int32 [T, k]) for the
  * context's E, k and n_shared, in stream order, into caller buffers (device

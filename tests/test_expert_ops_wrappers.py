@@ -183,3 +183,8 @@ def test_a_graph_that_kept_an_overwritten_tensor_notices(no_library, name):
     for k in kept:
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             k.float().sum().backward()
+
+
+def test_status_of_the_operators_without_a_gpu():
+    if not torch.cuda.is_available():
+        assert moe.moe_ops_status(None) == moe.MOE_ERR_CUDA
