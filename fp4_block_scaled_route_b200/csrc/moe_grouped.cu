@@ -19,8 +19,9 @@
 // the L2 delivers little more than that: with a quarter of the loads left out
 // the dense product took 320 us instead of 352.  32 ragged groups of 32768
 // rows, 4096 x 7168: 1643 us, 1.17 PFLOP/s, about 1.1 GHz at 1000 W (cuBLAS
-// sustains 1.40 on a dense product of that size); dense 8192 rows: 325 us,
-// 1.48 PFLOP/s (cuBLAS 310 us).  8-bit: 8192 x 4096 x 7168 159 us, 3.0 POP/s.
+// sustains 1.40 on a dense product of that size); dense 8192 rows: 302 to 334
+// us, 1.59 to 1.44 PFLOP/s (cuBLAS 303 to 326).  8-bit: 8192 x 4096 x 7168 159
+// us, 3.0 POP/s.
 #include "moe_grouped.cuh"
 
 namespace moe {

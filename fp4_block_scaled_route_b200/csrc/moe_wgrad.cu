@@ -2,11 +2,11 @@
 // dW_e[n, k] = sum over the rows p of group e of dy[p, n] x[p, k].
 //
 // What bounds it: for long groups the tensor cores and the loads that feed
-// them (dense, 8192 rows into 4096 x 7168: 343 us, 1.40 PFLOP/s; cuBLAS
-// 342 us), for groups of a few hundred rows also the result's way out (32
-// groups of 512 rows into 2048 x 7168 bf16, 940 MB: 498 us), for short ones
-// that alone (64 groups of 16 rows into 392 x 1032 fp32, 104 MB: 37 us, 2.9
-// TB/s; a plain fill reaches 3.9).
+// them (dense, 8192 rows into 4096 x 7168: 324 to 363 us, 1.48 to 1.32
+// PFLOP/s; cuBLAS 333 to 360), for groups of a few hundred rows also the
+// result's way out (32 groups of 512 rows into 2048 x 7168 bf16, 940 MB: 497
+// us), for short ones that alone (64 groups of 16 rows into 392 x 1032 fp32,
+// 104 MB: 37 us, 2.9 TB/s; a fill reaches 6.2).
 #include <type_traits>
 
 #include "moe_grouped.cuh"

@@ -435,8 +435,14 @@ moe_status moe_forward_noalloc(int H, int I, int E, int k, int wfmt, int n_share
  *     NULL: these errors go to the current device's word, which
  *     moe_ops_status() reads.
  *   - Sizes past P <= 2^24 rows or N, K <= 2^20: MOE_ERR_UNSUPPORTED.
- *   - Sums are held in fp32 (int8 products: exact int32) and rounded once,
- *     to nearest even, to the output type. */
+ *   - Sums are held in fp32 and rounded once, to nearest even, to the output
+ *     type.  The tensor cores truncate additions within segments of a
+ *     contraction, which are then added with rounding; whatever the length,
+ *     with terms of one sign, relative to the sum: into fp32 1e-6 (bf16
+ *     operands) or 6e-6 (fp16), into fp16 5e-5, into bf16 2e-4 (a tenth and a
+ *     twentieth of half a step of these types).  Int8 products: exact int32
+ *     sums, converted to fp32 and multiplied by the row's and then the
+ *     column's scale, each rounded in fp32 before the output's rounding. */
 
 /* Element types. */
 enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 };
